@@ -1,0 +1,254 @@
+// Host side of the key/value cache: validation, workspace, choice of the kernel
+// and of the split over the keys.
+#include <math.h>
+
+#include <algorithm>
+#include <new>
+
+#include "../../include/librescomp_kv.h"
+#include "kv.hpp"
+
+struct rc_kv_plan {
+  rc_kv_shape_t shape;
+  rc_dtype_t dtype;
+  rc_kv_params_t params;
+  void* ws = nullptr;  // partial outputs of a split, then their (m, l)
+  size_t ws_bytes = 0;
+};
+
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// How a call runs: which kernel, over how many parts of the keys.
+struct Way {
+  bool few;
+  int splits;
+  int64_t part_rows;  // rows of partial results; 0 with one split
+};
+
+Way way_of(const rc_kv_plan* pl, int64_t queries, int64_t blocks, bool chosen) {
+  const rc_kv_shape_t& s = pl->shape;
+  const int64_t group = s.q_heads / s.kv_heads, rows = queries * group;
+  const bool own_lists = chosen && pl->params.q_tile == 1;
+  Way w;
+  w.few = own_lists || rows <= 64;
+  const int64_t heads = (int64_t)s.batch * s.kv_heads;
+  int64_t splits = 1;
+  if (w.few) {
+    const int64_t base = heads * (own_lists ? queries * ceil_div(group, 16) : ceil_div(rows, 16));
+    splits = std::min(ceil_div(1024, base), ceil_div(blocks, 4));
+  } else {
+    const int64_t base = heads * ceil_div(rows, 128);
+    if (base < 384) splits = std::min(ceil_div(512, base), ceil_div(blocks, 8));
+  }
+  w.splits = (int)std::max<int64_t>(splits, 1);
+  w.part_rows = w.splits > 1 ? w.splits * heads * rows : 0;
+  return w;
+}
+
+size_t part_bytes(const rc_kv_plan* pl, int64_t part_rows) {
+  return (size_t)part_rows * ((size_t)pl->shape.head_dim * 4 + sizeof(float2));
+}
+
+rc_status_t check(const rc_kv_shape_t& s, rc_dtype_t dtype, const rc_kv_params_t* p) {
+  if (!p) return RC_ERR_INVALID_ARG;
+  if (s.batch < 1 || s.q_heads < 1 || s.kv_heads < 1 || s.head_dim < 1 || s.pool_blocks < 1 || s.seq_blocks < 1)
+    return RC_ERR_INVALID_ARG;
+  if (s.q_heads % s.kv_heads) return RC_ERR_INVALID_ARG;
+  if (dtype != RC_BF16 && dtype != RC_F32) return RC_ERR_INVALID_ARG;
+  if (p->max_queries < 1 || !(p->scale >= 0.0f) || !isfinite(p->scale)) return RC_ERR_INVALID_ARG;
+  if (p->flags & ~RC_KV_CAUSAL) return RC_ERR_INVALID_ARG;
+  if (p->q_tile != 0 && p->q_tile != 1 && p->q_tile != RC_KV_QTILE)
+    return p->q_tile < 0 ? RC_ERR_INVALID_ARG : RC_ERR_UNSUPPORTED;
+  if (p->q_tile == 0 ? p->keep_blocks != 0 : p->keep_blocks < 1) return RC_ERR_INVALID_ARG;
+  if (p->q_tile == RC_KV_QTILE && (p->flags & RC_KV_CAUSAL) && p->keep_blocks < 3) return RC_ERR_INVALID_ARG;
+  if (p->keep_blocks > 1024) return RC_ERR_UNSUPPORTED;
+  if (s.head_dim != 64 && s.head_dim != 128) return RC_ERR_UNSUPPORTED;
+  if (s.batch > 65535 || s.kv_heads > 32767 || s.seq_blocks > RC_KV_MAX_BLOCKS) return RC_ERR_UNSUPPORTED;
+  if ((int64_t)p->max_queries * s.q_heads >= (int64_t)1 << 30) return RC_ERR_UNSUPPORTED;
+  if ((int64_t)s.batch * s.seq_blocks >= (int64_t)1 << 31) return RC_ERR_UNSUPPORTED;
+  return RC_OK;
+}
+
+bool at16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool at4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+rc_status_t check_cache(const rc_kv_cache_t* c) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !c->k_mean || !c->k_mean_scale) return RC_ERR_INVALID_ARG;
+  if (!at16(c->k) || !at16(c->v) || !at16(c->k_scale) || !at16(c->v_scale) || !at16(c->k_mean) ||
+      !at16(c->k_mean_scale))
+    return RC_ERR_ALIGNMENT;
+  return RC_OK;
+}
+
+// A view of [batch][tokens][heads][dim]; strides of dimensions of size 1 do not count.
+rc_status_t rows_of(const rc_kv_view_t* v, int64_t batch, int64_t tokens, int64_t heads, int64_t dim, bool out,
+                    rc::KvRows* r) {
+  if (!v || (!v->data && tokens > 0)) return RC_ERR_INVALID_ARG;
+  if (v->dtype != RC_BF16 && v->dtype != RC_F32) return RC_ERR_INVALID_ARG;
+  if (!at16(v->data)) return RC_ERR_ALIGNMENT;
+  const int64_t unit = v->dtype == RC_BF16 ? 8 : 4, n[3] = {batch, tokens, heads};
+  int64_t st[3] = {v->batch_stride, v->token_stride, v->head_stride};
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] <= 1) st[i] = 0;
+    else if (st[i] < (out ? dim : 0) || st[i] >= (int64_t)1 << 40) return RC_ERR_INVALID_ARG;
+    if (st[i] % unit) return RC_ERR_ALIGNMENT;
+  }
+  *r = {v->data, st[0], st[1], st[2]};
+  return RC_OK;
+}
+
+rc::KvGeom geometry(const rc_kv_plan* pl, const rc_kv_cache_t* c, const int32_t* table) {
+  const rc_kv_shape_t& s = pl->shape;
+  rc::KvGeom g;
+  g.k = static_cast<uint8_t*>(c->k);
+  g.v = static_cast<uint8_t*>(c->v);
+  g.k_scale = c->k_scale;
+  g.v_scale = c->v_scale;
+  g.k_mean = c->k_mean;
+  g.k_mean_scale = c->k_mean_scale;
+  g.table = table;
+  g.batch = s.batch;
+  g.q_heads = s.q_heads;
+  g.kv_heads = s.kv_heads;
+  g.dim = s.head_dim;
+  g.group = s.q_heads / s.kv_heads;
+  g.pool_blocks = s.pool_blocks;
+  g.seq_blocks = s.seq_blocks;
+  return g;
+}
+
+// What rc_kv_select and rc_kv_attend check alike.
+rc_status_t prepare(rc_kv_plan* pl, const rc_kv_cache_t* cache, const int32_t* table, const int32_t* kv_len,
+                    int64_t max_len, int queries, const rc_kv_view_t* q, rc::KvAttendArgs* a) {
+  if (!pl || !kv_len || queries < 0 || queries > pl->params.max_queries || max_len < 0) return RC_ERR_INVALID_ARG;
+  if (!at4(kv_len) || (table && !at4(table))) return RC_ERR_ALIGNMENT;
+  rc_status_t st = check_cache(cache);
+  if (st != RC_OK) return st;
+  const rc_kv_shape_t& s = pl->shape;
+  st = rows_of(q, s.batch, queries, s.q_heads, s.head_dim, false, &a->q);
+  if (st != RC_OK) return st;
+  if (q->dtype != pl->dtype) return RC_ERR_INVALID_ARG;
+  a->g = geometry(pl, cache, table);
+  a->kv_len = kv_len;
+  const int64_t cap = (int64_t)RC_KV_BLOCK * s.seq_blocks;
+  a->max_len = (int)(max_len == 0 ? cap : std::min(max_len, cap));
+  a->queries = queries;
+  a->causal = (pl->params.flags & RC_KV_CAUSAL) != 0;
+  a->q_tile = pl->params.q_tile;
+  a->keep = pl->params.keep_blocks;
+  a->tiles = a->q_tile ? (int)ceil_div(queries, a->q_tile) : 0;
+  a->scale = pl->params.scale > 0.0f ? pl->params.scale : 1.0f / sqrtf((float)s.head_dim);
+  a->lse = nullptr;
+  a->blocks = nullptr;
+  a->blocks_out = nullptr;
+  a->splits = 1;
+  a->part = nullptr;
+  a->part_ml = nullptr;
+  a->out = {nullptr, 0, 0, 0};
+  return RC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+rc_status_t rc_kv_plan_create(rc_kv_shape_t shape, rc_dtype_t dtype, const rc_kv_params_t* params,
+                              rc_kv_plan_t* out) {
+  if (!out) return RC_ERR_INVALID_ARG;
+  *out = nullptr;
+  const rc_status_t st = check(shape, dtype, params);
+  if (st != RC_OK) return st;
+  rc_kv_plan* pl = new (std::nothrow) rc_kv_plan;
+  if (!pl) return RC_ERR_HIP;
+  pl->shape = shape;
+  pl->dtype = dtype;
+  pl->params = *params;
+  // the most that any number of queries needs (fewer blocks mean fewer splits);
+  // more queries than this are never split
+  int64_t most = 0;
+  const int64_t top = std::min<int64_t>(params->max_queries, 65536);
+  for (int64_t q = 1; q <= top; ++q) {
+    most = std::max(most, way_of(pl, q, shape.seq_blocks, false).part_rows);
+    if (params->q_tile) most = std::max(most, way_of(pl, q, params->keep_blocks, true).part_rows);
+  }
+  pl->ws_bytes = part_bytes(pl, most);
+  if (pl->ws_bytes && hipMalloc(&pl->ws, pl->ws_bytes) != hipSuccess) {
+    delete pl;
+    return RC_ERR_HIP;
+  }
+  *out = pl;
+  return RC_OK;
+}
+
+rc_status_t rc_kv_store(rc_kv_plan_t pl, hipStream_t stream, const rc_kv_cache_t* cache, const int32_t* table,
+                        const int32_t* start, const int32_t* count, int tokens, const rc_kv_view_t* k,
+                        const rc_kv_view_t* v) {
+  if (!pl || !start || tokens < 0) return RC_ERR_INVALID_ARG;
+  if (!at4(start) || (table && !at4(table)) || (count && !at4(count))) return RC_ERR_ALIGNMENT;
+  rc_status_t st = check_cache(cache);
+  if (st != RC_OK) return st;
+  const rc_kv_shape_t& s = pl->shape;
+  rc::KvStoreArgs a;
+  st = rows_of(k, s.batch, tokens, s.kv_heads, s.head_dim, false, &a.k);
+  if (st == RC_OK) st = rows_of(v, s.batch, tokens, s.kv_heads, s.head_dim, false, &a.v);
+  if (st != RC_OK) return st;
+  if (tokens == 0) return RC_OK;
+  a.g = geometry(pl, cache, table);
+  a.start = start;
+  a.count = count;
+  a.tokens = tokens;
+  return rc::launch_kv_store(a, k->dtype == RC_BF16, v->dtype == RC_BF16, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
+}
+
+rc_status_t rc_kv_select(rc_kv_plan_t pl, hipStream_t stream, const rc_kv_cache_t* cache, const int32_t* table,
+                         const int32_t* kv_len, int64_t max_len, int queries, const rc_kv_view_t* q,
+                         int32_t* blocks) {
+  rc::KvAttendArgs a;
+  const rc_status_t st = prepare(pl, cache, table, kv_len, max_len, queries, q, &a);
+  if (st != RC_OK) return st;
+  if (!blocks || !a.q_tile) return RC_ERR_INVALID_ARG;
+  if (!at4(blocks)) return RC_ERR_ALIGNMENT;
+  if (queries == 0) return RC_OK;
+  a.blocks_out = blocks;
+  return rc::launch_kv_select(a, pl->dtype == RC_BF16, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
+}
+
+rc_status_t rc_kv_attend(rc_kv_plan_t pl, hipStream_t stream, const rc_kv_cache_t* cache, const int32_t* table,
+                         const int32_t* kv_len, int64_t max_len, int queries, const rc_kv_view_t* q,
+                         const int32_t* blocks, const rc_kv_view_t* out, float* lse) {
+  rc::KvAttendArgs a;
+  rc_status_t st = prepare(pl, cache, table, kv_len, max_len, queries, q, &a);
+  if (st != RC_OK) return st;
+  const rc_kv_shape_t& s = pl->shape;
+  st = rows_of(out, s.batch, queries, s.q_heads, s.head_dim, true, &a.out);
+  if (st != RC_OK) return st;
+  if (out->dtype != pl->dtype || (blocks && !a.q_tile)) return RC_ERR_INVALID_ARG;
+  if ((lse && !at4(lse)) || (blocks && !at4(blocks))) return RC_ERR_ALIGNMENT;
+  if (queries == 0) return RC_OK;
+  a.lse = lse;
+  a.blocks = blocks;
+  int64_t reach = ceil_div(a.max_len, RC_KV_BLOCK);
+  if (blocks) reach = std::min<int64_t>(reach, a.keep);
+  const Way w = way_of(pl, queries, reach, blocks != nullptr);
+  a.splits = w.splits;
+  if (w.splits > 1) {
+    if (part_bytes(pl, w.part_rows) > pl->ws_bytes) return RC_ERR_INVALID_ARG;  // not reached: sized for it
+    a.part = static_cast<float*>(pl->ws);
+    a.part_ml = reinterpret_cast<float2*>(a.part + w.part_rows * s.head_dim);
+  }
+  return rc::launch_kv_attend(a, w.few, pl->dtype == RC_BF16, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
+}
+
+rc_status_t rc_kv_plan_destroy(rc_kv_plan_t pl) {
+  if (!pl) return RC_OK;
+  hipError_t err = hipSuccess;
+  if (pl->ws) err = hipFree(pl->ws);
+  delete pl;
+  return err == hipSuccess ? RC_OK : RC_ERR_HIP;
+}
+
+size_t rc_kv_workspace_bytes(rc_kv_plan_t pl) { return pl ? pl->ws_bytes : 0; }
+
+}  // extern "C"

@@ -53,6 +53,29 @@ class rc_state_t(ctypes.Structure):
     _fields_ = [("ahat", ctypes.c_void_p), ("e", ctypes.c_void_p)]
 
 
+RC_KV_BLOCK, RC_KV_QTILE, RC_KV_MAX_BLOCKS = 64, 128, 8192  # librescomp_kv.h
+RC_KV_CAUSAL = 1  # rc_kv_params_t.flags
+
+
+class rc_kv_shape_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "q_heads", "kv_heads", "head_dim", "pool_blocks",
+                                              "seq_blocks")]
+
+
+class rc_kv_params_t(ctypes.Structure):
+    _fields_ = [("max_queries", ctypes.c_int32), ("scale", ctypes.c_float), ("q_tile", ctypes.c_int32),
+                ("keep_blocks", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class rc_kv_cache_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "k_mean", "k_mean_scale")]
+
+
+class rc_kv_view_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("batch_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
 class RcError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -88,6 +111,20 @@ def _load():
     for f in ("rc_packed_bytes", "rc_tensor_packed_bytes", "rc_workspace_bytes"):
         getattr(lib, f).restype = sz
         getattr(lib, f).argtypes = [vp]
+    lib.rc_kv_plan_create.restype = st
+    lib.rc_kv_plan_create.argtypes = [rc_kv_shape_t, ctypes.c_int, ctypes.POINTER(rc_kv_params_t),
+                                      ctypes.POINTER(vp)]
+    cache, view = ctypes.POINTER(rc_kv_cache_t), ctypes.POINTER(rc_kv_view_t)
+    lib.rc_kv_store.restype = st
+    lib.rc_kv_store.argtypes = [vp, vp, cache, vp, vp, vp, ctypes.c_int, view, view]
+    lib.rc_kv_select.restype = st
+    lib.rc_kv_select.argtypes = [vp, vp, cache, vp, vp, ctypes.c_int64, ctypes.c_int, view, vp]
+    lib.rc_kv_attend.restype = st
+    lib.rc_kv_attend.argtypes = [vp, vp, cache, vp, vp, ctypes.c_int64, ctypes.c_int, view, vp, view, vp]
+    lib.rc_kv_plan_destroy.restype = st
+    lib.rc_kv_plan_destroy.argtypes = [vp]
+    lib.rc_kv_workspace_bytes.restype = sz
+    lib.rc_kv_workspace_bytes.argtypes = [vp]
     lib.rc_status_string.restype = ctypes.c_char_p
     lib.rc_status_string.argtypes = [ctypes.c_int]
     lib.rcx_lowrank_workspace.restype = ctypes.c_int
@@ -355,6 +392,188 @@ class Plan:
     def close(self):
         if self.handle is not None:
             rc_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+# ------------------------------------------------------------------ 8-bit key/value cache
+def rc_kv_plan_create(shape, dtype, params: rc_kv_params_t):
+    """shape: rc_kv_shape_t or its fields in order; dtype: enum int or name."""
+    if not isinstance(shape, rc_kv_shape_t):
+        shape = rc_kv_shape_t(*shape)
+    plan = ctypes.c_void_p()
+    _check(_lib.rc_kv_plan_create(shape, int(DTYPES.get(dtype, dtype)), ctypes.byref(params), ctypes.byref(plan)),
+           "rc_kv_plan_create")
+    return plan
+
+
+def rc_kv_store(plan, stream, cache: rc_kv_cache_t, table, start, count, tokens, k: rc_kv_view_t, v: rc_kv_view_t):
+    _check(_lib.rc_kv_store(plan, _stream(stream), ctypes.byref(cache), _ptr(table), _ptr(start), _ptr(count),
+                            int(tokens), ctypes.byref(k), ctypes.byref(v)), "rc_kv_store")
+
+
+def rc_kv_select(plan, stream, cache: rc_kv_cache_t, table, kv_len, max_len, queries, q: rc_kv_view_t, blocks):
+    _check(_lib.rc_kv_select(plan, _stream(stream), ctypes.byref(cache), _ptr(table), _ptr(kv_len), int(max_len),
+                             int(queries), ctypes.byref(q), _ptr(blocks)), "rc_kv_select")
+
+
+def rc_kv_attend(plan, stream, cache: rc_kv_cache_t, table, kv_len, max_len, queries, q: rc_kv_view_t, blocks,
+                 out: rc_kv_view_t, lse):
+    _check(_lib.rc_kv_attend(plan, _stream(stream), ctypes.byref(cache), _ptr(table), _ptr(kv_len), int(max_len),
+                             int(queries), ctypes.byref(q), _ptr(blocks), ctypes.byref(out), _ptr(lse)),
+           "rc_kv_attend")
+
+
+def rc_kv_plan_destroy(plan):
+    _check(_lib.rc_kv_plan_destroy(plan), "rc_kv_plan_destroy")
+
+
+def rc_kv_workspace_bytes(plan) -> int:
+    return int(_lib.rc_kv_workspace_bytes(plan))
+
+
+class KvCache:
+    """The tensors of an 8-bit key/value cache (librescomp_kv.h), the caller's:
+    k [pool, heads, D/16, 64, 16] and v [pool, heads, 4, D, 16] of one byte an
+    element (float8_e4m3fn, or uint8), k_scale, v_scale and k_mean_scale fp32
+    [pool, heads], k_mean int8 [pool, heads, D], all contiguous on the GPU."""
+
+    def __init__(self, k, v, k_scale, v_scale, k_mean, k_mean_scale):
+        self.pool_blocks, self.kv_heads, chunks = (int(n) for n in k.shape[:3])
+        self.head_dim = 16 * chunks
+        row = (self.pool_blocks, self.kv_heads)
+        for what, x, shape, types in (
+                ("k", k, row + (chunks, RC_KV_BLOCK, 16), ("torch.float8_e4m3fn", "torch.uint8")),
+                ("v", v, row + (4, self.head_dim, 16), ("torch.float8_e4m3fn", "torch.uint8")),
+                ("k_scale", k_scale, row, ("torch.float32",)), ("v_scale", v_scale, row, ("torch.float32",)),
+                ("k_mean", k_mean, row + (self.head_dim,), ("torch.int8",)),
+                ("k_mean_scale", k_mean_scale, row, ("torch.float32",))):
+            if tuple(x.shape) != shape:
+                raise ValueError("%s is %s, a cache of this k has %s" % (what, tuple(x.shape), shape))
+            if str(x.dtype) not in types:
+                raise ValueError("%s is %s, the cache takes %s" % (what, x.dtype, " or ".join(types)))
+        for what, x in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale), ("k_mean", k_mean),
+                        ("k_mean_scale", k_mean_scale)):
+            _dev_buffer(x, 0, what)
+        self.k, self.v, self.k_scale, self.v_scale, self.k_mean, self.k_mean_scale = \
+            k, v, k_scale, v_scale, k_mean, k_mean_scale
+        self.struct = rc_kv_cache_t(*(x.data_ptr() for x in (k, v, k_scale, v_scale, k_mean, k_mean_scale)))
+        self.geometry = (self.pool_blocks, self.kv_heads, self.head_dim)
+
+    @classmethod
+    def empty(cls, pool_blocks, kv_heads, head_dim, device="cuda"):
+        """A cache that holds nothing (all zero)."""
+        import torch
+        row = (pool_blocks, kv_heads)
+
+        def zeros(shape, dtype):
+            return torch.zeros(shape, dtype=dtype, device=device)
+        return cls(zeros(row + (head_dim // 16, RC_KV_BLOCK, 16), torch.uint8).view(torch.float8_e4m3fn),
+                   zeros(row + (4, head_dim, 16), torch.uint8).view(torch.float8_e4m3fn),
+                   zeros(row, torch.float32) + 1.0, zeros(row, torch.float32) + 1.0,
+                   zeros(row + (head_dim,), torch.int8), zeros(row, torch.float32))
+
+
+class KvPlan:
+    """Owns one rc_kv_plan_t; a thin wrapper over the calls above that checks what
+    it is given. Tensors are [batch, tokens, heads, head_dim] with contiguous rows
+    (any strides between them)."""
+
+    def __init__(self, batch, q_heads, kv_heads, head_dim, pool_blocks, seq_blocks, dtype="bf16", max_queries=1,
+                 causal=False, scale=0.0, q_tile=0, keep_blocks=0):
+        self.batch, self.q_heads, self.kv_heads, self.head_dim = int(batch), int(q_heads), int(kv_heads), int(head_dim)
+        self.seq_blocks, self.q_tile, self.keep_blocks = int(seq_blocks), int(q_tile), int(keep_blocks)
+        self.geometry = (int(pool_blocks), self.kv_heads, self.head_dim)
+        params = rc_kv_params_t(int(max_queries), float(scale), self.q_tile, self.keep_blocks,
+                                RC_KV_CAUSAL if causal else 0)
+        self.handle = None
+        self.dtype = DTYPES.get(dtype, dtype)
+        self.handle = rc_kv_plan_create((self.batch, self.q_heads, self.kv_heads, self.head_dim, int(pool_blocks),
+                                         self.seq_blocks), self.dtype, params)
+        self.workspace_bytes = rc_kv_workspace_bytes(self.handle)
+
+    def _rows(self, x, heads, what, tokens=None, dtype=None):
+        """View of x, checked for device, shape and type."""
+        import torch
+        if not x.is_cuda:
+            raise ValueError("%s must be a device tensor" % what)
+        shape = x.shape
+        if len(shape) != 4 or shape[0] != self.batch or shape[2] != heads or shape[3] != self.head_dim or \
+                (tokens is not None and shape[1] != tokens):
+            raise ValueError("%s is %s, the call takes (%d, %s, %d, %d)" % (
+                what, tuple(shape), self.batch, "tokens" if tokens is None else tokens, heads, self.head_dim))
+        code = RC_BF16 if x.dtype is torch.bfloat16 else RC_F32 if x.dtype is torch.float32 else None
+        if code is None or (dtype is not None and code != dtype):
+            raise ValueError("%s is %s, the call takes %s" % (what, x.dtype, {
+                None: "bfloat16 or float32", RC_BF16: "bfloat16", RC_F32: "float32"}[dtype]))
+        b, t, h, d = x.stride()
+        if d != 1:
+            raise ValueError("%s must have contiguous rows of head_dim" % what)
+        return rc_kv_view_t(x.data_ptr(), code, b, t, h)
+
+    def _ints(self, x, n, what):
+        if x is None:
+            return None
+        import torch
+        if hasattr(x, "data_ptr"):
+            if x.dtype is not torch.int32 or not x.is_cuda or not x.is_contiguous() or x.numel() != n:
+                raise ValueError("%s must be a contiguous int32 device tensor of %d values" % (what, n))
+        return _ptr(x)
+
+    def _cache(self, cache):
+        if cache.geometry != self.geometry:
+            raise ValueError("the cache has (blocks, heads, head_dim) %s, the plan %s" % (cache.geometry, self.geometry))
+        return cache.struct
+
+    def store(self, cache, start, k, v, table=None, count=None, stream=None):
+        """Quantise k, v [batch, tokens, kv_heads, head_dim] into the cache, from
+        position start[b] of each sequence on."""
+        tokens = k.shape[1]
+        kv, vv = self._rows(k, self.kv_heads, "k"), self._rows(v, self.kv_heads, "v", tokens)
+        rc_kv_store(self.handle, stream, self._cache(cache), self._ints(table, self.batch * self.seq_blocks, "table"),
+                    self._ints(start, self.batch, "start"), self._ints(count, self.batch, "count"), tokens, kv, vv)
+
+    def _lists(self, blocks, queries):
+        tiles = -(-queries // self.q_tile) if self.q_tile else 0
+        return self._ints(blocks, self.batch * self.kv_heads * tiles * self.keep_blocks, "blocks")
+
+    def select(self, cache, kv_len, q, blocks, table=None, max_len=0, stream=None):
+        """Choose blocks for q [batch, queries, q_heads, head_dim]; writes blocks, int32
+        [batch, kv_heads, ceil(queries / q_tile), keep_blocks]."""
+        queries = q.shape[1]
+        view = self._rows(q, self.q_heads, "q", None, self.dtype)
+        rc_kv_select(self.handle, stream, self._cache(cache), self._ints(table, self.batch * self.seq_blocks, "table"),
+                     self._ints(kv_len, self.batch, "kv_len"), max_len, queries, view, self._lists(blocks, queries))
+
+    def attend(self, cache, kv_len, q, out, lse=None, table=None, max_len=0, blocks=None, stream=None):
+        """Attention of q over the cache (over the chosen blocks, if given); writes out,
+        like q, and lse, fp32 [batch, queries, q_heads]."""
+        queries = q.shape[1]
+        view = self._rows(q, self.q_heads, "q", None, self.dtype)
+        to = self._rows(out, self.q_heads, "out", queries, self.dtype)
+        if lse is not None:
+            import torch
+            if hasattr(lse, "dtype") and (lse.dtype is not torch.float32 or lse.numel() != self.batch * queries * self.q_heads):
+                raise ValueError("lse must hold %d fp32 values" % (self.batch * queries * self.q_heads))
+            lse = _dev_buffer(lse, 0, "lse")
+        rc_kv_attend(self.handle, stream, self._cache(cache), self._ints(table, self.batch * self.seq_blocks, "table"),
+                     self._ints(kv_len, self.batch, "kv_len"), max_len, queries, view, self._lists(blocks, queries), to,
+                     lse)
+
+    def close(self):
+        if self.handle is not None:
+            rc_kv_plan_destroy(self.handle)
             self.handle = None
 
     def __del__(self):
