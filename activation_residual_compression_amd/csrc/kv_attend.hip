@@ -9,8 +9,10 @@
 // of two f16 for fp32. Scores, statistics and outputs are accumulated in fp32.
 //
 // Softmax in base 2: with c = scale * log2(e) * (scale of the row and block),
-// p = 2^(S c - m + kBias), m the running maximum of S c. kBias lifts small
-// probabilities out of f16's subnormals; it cancels in out = O / l.
+// p = 2^(S c - m + kBias), m the running maximum of S c (in the kernel for many rows
+// only followed when p no longer fits f16, so the accumulators are rescaled a few
+// times in all and not at every block). kBias lifts small probabilities out of f16's
+// subnormals; both cancel in out = O / l.
 //
 // V's exponent ev differs from block to block. The output accumulators hold units
 // of 2^ev_cur: while ev is near ev_cur the difference goes into the exponent of p
@@ -30,7 +32,7 @@ namespace rc {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr float kBias = 8.0f;      // p <= 2^(8 + 2): f16 holds 2^15
+constexpr float kBias = 7.0f, kMost = 0x1p15f;  // f16 holds 2^15
 constexpr int kEvUp = 2, kEvDown = 8;
 constexpr float kLowest = -3.402823466e38f;
 
@@ -86,6 +88,25 @@ __device__ __forceinline__ int list_length(const int32_t* list, int keep, int re
   }
   return keep;
 }
+
+// Takes in probability e of 16 (in order): the sum, and when it closes a pair, f16
+// (and for fp32 what that left). Pinned in place: see the step of the many-row kernel.
+template <bool F32>
+__device__ __forceinline__ void take_p(const float (&p)[16], int e, float& sum, u32x4 (&ph)[2], u32x4 (&pl)[2]) {
+  sum += p[e];
+  if (e % 2 == 0) return;
+  const half2_t hi = {(_Float16)p[e - 1], (_Float16)p[e]};
+  uint32_t w = __builtin_bit_cast(uint32_t, hi);
+  if constexpr (F32) {
+    const half2_t lo = {(_Float16)(p[e - 1] - (float)hi.x), (_Float16)(p[e] - (float)hi.y)};
+    uint32_t v = __builtin_bit_cast(uint32_t, lo);
+    asm volatile("" : "+v"(v));
+    pl[e / 8][e % 8 / 2] = v;
+  }
+  asm volatile("" : "+v"(w), "+v"(sum));
+  ph[e / 8][e % 8 / 2] = w;
+}
+__device__ __forceinline__ half8_t as_half8(u32x4 x) { return __builtin_bit_cast(half8_t, x); }
 
 // Keeps the first n of the 16 codes of u (n <= 0: none), so that stale codes after
 // a sequence's end never meet a probability of zero as a NaN.
@@ -300,22 +321,111 @@ __global__ __launch_bounds__(256, 2) void kv_attend_few_kernel(KvAttendArgs a) {
 }
 
 // ------------------------------------------------------------------ many rows
+// The blocks that a part of a call reads, one after the other, without a load in
+// the way: the wave's 64 lanes hold the next 64 entries (index, pool block, scales),
+// loaded at once, and hand them out one by one. Blocks that do not exist are skipped.
+struct Walk {
+  const KvGeom& g;
+  const int32_t* list;
+  int b, h, base, to, lane;
+  uint64_t left;  // entries of this 64 still to come
+  int lane_j, lane_block;
+  float lane_ks, lane_vs;
+
+  __device__ __forceinline__ Walk(const KvGeom& g, const int32_t* list, int b, int h, int from, int to, int lane)
+      : g(g), list(list), b(b), h(h), base(from - 64), to(to), lane(lane), left(0) {}
+  __device__ __forceinline__ void fill() {
+    base += 64;
+    lane_block = -1;
+    if (base + lane < to) {
+      lane_j = list ? list[base + lane] : base + lane;
+      lane_block = kv_block(g, b, lane_j);
+      if (lane_block >= 0) {
+        lane_ks = g.k_scale[kv_row(g, lane_block, h)];
+        lane_vs = g.v_scale[kv_row(g, lane_block, h)];
+      }
+    }
+    left = __ballot(lane_block >= 0);
+  }
+  // The next block: its index j (-1: none), pool block and scales.
+  __device__ __forceinline__ int next(int& block, float& ks, int& ev) {
+    while (left == 0) {
+      if (base + 64 >= to) return -1;
+      fill();
+    }
+    const int i = __builtin_ctzll(left);
+    left &= left - 1;
+    block = __builtin_amdgcn_readlane(lane_block, i);
+    ks = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(lane_ks), i));
+    ev = scale_exponent(__uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(lane_vs), i)));
+    return __builtin_amdgcn_readlane(lane_j, i);
+  }
+};
+
+// Which part of the call a block of threads does. They go to the 8 XCDs in turn, so
+// where the load of the XCDs stays even, a key head's row tiles are given to one XCD,
+// whose L2 then holds its K and V: with a multiple of 8 key heads, head h to XCD h % 8
+// (every XCD gets the same share of every sequence, however long); with one sequence
+// whose rows all see the same, equal runs of the heads' tiles. Otherwise the tiles are
+// in order of length, the longest first, over all heads. Measured on 1152 queries over
+// 4608 tokens (2 x 24 heads of 128): 140 us, against 147 in plain order; the runs on
+// three ragged causal sequences of 4 key heads: 195 us against 115 in plain order.
+struct Place {
+  int b, h, split, tile;
+};
+__device__ __forceinline__ Place place_of(const KvAttendArgs& a, uint32_t w, uint32_t grid, int row_tiles) {
+  const uint32_t per = (uint32_t)(row_tiles * a.splits), heads = (uint32_t)a.g.kv_heads;
+  uint32_t in_head, b, h;
+  if (heads % 8 == 0) {
+    const uint32_t xcd = w & 7u;
+    w >>= 3;
+    in_head = w % per;
+    w /= per;
+    h = w % (heads / 8) * 8 + xcd;
+    b = w / (heads / 8);
+  } else if (!a.causal && a.g.batch == 1) {
+    const uint32_t xcd = w & 7u;
+    w = xcd * (grid >> 3) + min(xcd, grid & 7u) + (w >> 3);
+    in_head = w % per;
+    h = w / per;
+    b = 0;
+  } else {
+    const uint32_t all = heads * (uint32_t)a.g.batch;
+    in_head = w / (all * a.splits) * a.splits + w % (uint32_t)a.splits;
+    w = w / a.splits % all;
+    h = w % heads;
+    b = w / heads;
+  }
+  const int tile = (int)in_head / a.splits;
+  return {(int)b, (int)h, (int)in_head % a.splits, a.causal ? row_tiles - 1 - tile : tile};
+}
+
+// The larger of a lane's value and that of the lane 32 away.
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 // One block of threads: 128 rows of one key head (32 a wave). K and V of a block
-// are widened to f16 once, on their way into LDS (two buffers: the next block's
-// loads are in flight while this one is computed), in the order of the operands,
-// so that every LDS read is one run of 64 lanes x 16 B.
+// are widened to f16 once, on their way into LDS, in the order of the operands, so
+// that every LDS read is one run of 64 lanes x 16 B.
+//
+// The matrix units and the exponentials take about as long as each other, so a wave
+// works on three half blocks (32 tokens) at once: the second product of half x - 1,
+// the softmax of half x and the first product of half x + 1 do not depend on each
+// other and are interleaved. K is therefore one block ahead of V in LDS (two buffers
+// of each, one barrier a block), and the global loads are one block ahead of that.
 template <int D, bool F32>
-__global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) {
+__global__ __launch_bounds__(256, D == 128 && F32 ? 1 : 2) void kv_attend_many_kernel(KvAttendArgs a) {
   constexpr int NK = D / 16, ND = D / 32, UNITS = 64 * D / 16 / 256;
   typedef typename std::conditional<F32, float, uint16_t>::type IO;
   __shared__ half8_t sk[2][D / 8][64];  // [channel / 8][operand row]
   __shared__ half8_t sv[2][8][D];       // [token / 8][channel]
   const KvGeom& g = a.g;
-  const int b = blockIdx.z, h = blockIdx.y;
   const int rows = a.queries * g.group;
   const int row_tiles = (rows + 127) / 128;
-  const int split = blockIdx.x / row_tiles;
-  const int tile = a.causal ? row_tiles - 1 - blockIdx.x % row_tiles : blockIdx.x % row_tiles;  // long rows first
+  const Place place = place_of(a, blockIdx.x, gridDim.x, row_tiles);
+  const int b = place.b, h = place.h, split = place.split, tile = place.tile;
   const int r0 = tile * 128;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, half = lane >> 5;
   const int r = r0 + wave * 32 + col;
@@ -323,7 +433,7 @@ __global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) 
   const Row me = row_of(a, h, min(r, rows - 1));
   const int len = kv_length(a, b);
   const int lim = live ? kv_limit(a, len, me.query) : 0;
-  const int lim_lo = kv_limit(a, len, r0 / g.group);
+  const int lim_lo = r0 + 128 > rows ? 0 : kv_limit(a, len, r0 / g.group);
   const int lim_hi = kv_limit(a, len, (min(r0 + 128, rows) - 1) / g.group);
   const int32_t* list = nullptr;
   const int reach = (lim_hi + 63) / 64;  // no block from here on, whatever a list says
@@ -347,7 +457,7 @@ __global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) 
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
     }
-    top = fmaxf(top, __shfl_xor(top, 32));
+    top = max_halves(top);
     float up, down;
     row_scale(top, up, down);
     cq = down * (a.scale * kLog2e);
@@ -361,121 +471,214 @@ __global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) 
     }
   }
 
-  // the next block that exists, at or after it; -1 at the end
-  const auto next = [&](int& it, int& block) {
-    for (; it < to; ++it) {
-      const int j = list ? list[it] : it;
-      block = kv_block(g, b, j);
-      if (block >= 0) return j;
-    }
-    return -1;
-  };
   u32x4 kr[UNITS], vr[UNITS];
-  const auto load = [&](int block) {
-    const int64_t row = kv_row(g, block, h);
-#pragma unroll
-    for (int u = 0; u < UNITS; ++u) {
-      const int unit = tid + 256 * u, p = unit & 63;
-      const int t = (p & ~12) | (p & 4) << 1 | (p & 8) >> 1;  // operand row -> token: bits 2 and 3 change places
-      kr[u] = *reinterpret_cast<const u32x4*>(g.k + row * (64 * D) + ((unit & ~63) | t) * 16);
-      vr[u] = *reinterpret_cast<const u32x4*>(g.v + row * (64 * D) + unit * 16);
-    }
+  const auto load_k = [&](int block, int u) {
+    const int unit = tid + 256 * u, p = unit & 63;
+    const int t = (p & ~12) | (p & 4) << 1 | (p & 8) >> 1;  // operand row -> token: bits 2 and 3 change places
+    kr[u] = *reinterpret_cast<const u32x4*>(g.k + kv_row(g, block, h) * (64 * D) + ((unit & ~63) | t) * 16);
   };
-  const auto stage = [&](int buf, int j) {
-#pragma unroll
-    for (int u = 0; u < UNITS; ++u) {
-      const int unit = tid + 256 * u;
-      sk[buf][2 * (unit >> 6)][unit & 63] = codes8(kr[u][0], kr[u][1]);
-      sk[buf][2 * (unit >> 6) + 1][unit & 63] = codes8(kr[u][2], kr[u][3]);
-      u32x4 w = vr[u];
-      if (j * 64 + 64 > len) w = keep_codes(w, len - j * 64 - 16 * (unit / D));
-      sv[buf][2 * (unit / D)][unit % D] = codes8(w[0], w[1]);
-      sv[buf][2 * (unit / D) + 1][unit % D] = codes8(w[2], w[3]);
-    }
+  const auto load_v = [&](int block, int u) {
+    vr[u] = *reinterpret_cast<const u32x4*>(g.v + kv_row(g, block, h) * (64 * D) + (tid + 256 * u) * 16);
   };
-
+  // 8 of a unit's 16 codes, widened
+  const auto put_k = [&](int buf, int u, int part) {
+    const int unit = tid + 256 * u;
+    sk[buf][2 * (unit >> 6) + part][unit & 63] = codes8(kr[u][2 * part], kr[u][2 * part + 1]);
+  };
+  const auto put_v = [&](int buf, int u, int part) {
+    const int unit = tid + 256 * u;
+    sv[buf][2 * (unit / D) + part][unit % D] = codes8(vr[u][2 * part], vr[u][2 * part + 1]);
+  };
   f32x16 o[ND];
 #pragma unroll
   for (int d = 0; d < ND; ++d) o[d] = f32x16{};
   float m_run = kLowest, l_run = 0.0f;
-  int ev_cur = 0, it = from, block = -1, buf = 0;
-  int j = next(it, block);
-  if (j >= 0) {
-    load(block);
-    stage(0, j);
-  }
-  while (j >= 0) {
-    const int64_t row = kv_row(g, block, h);
-    const float ck = cq * g.k_scale[row];
-    float factor;
-    const int delta = enter_block(ev_cur, scale_exponent(g.v_scale[row]), factor);
-    int block_n = -1;
-    ++it;
-    const int j_n = next(it, block_n);
-    if (j_n >= 0) load(block_n);
-    __syncthreads();
+  int ev_cur = 0;
 
-    f32x16 s16[2];
+  // S^T of the first or second half of the block in sk[buf]
+  const auto first_product = [&](f32x16& s, int buf, int u) {
+    s = f32x16{};
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      s16[t] = f32x16{};
-#pragma unroll
-      for (int s = 0; s < NK; ++s) {
-        const half8_t kf = sk[buf][2 * s + half][32 * t + col];
-        s16[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qh[s], s16[t], 0, 0, 0);
-        if constexpr (F32) s16[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, ql[s], s16[t], 0, 0, 0);
-      }
+    for (int i = 0; i < NK; ++i) {
+      const half8_t kf = sk[buf][2 * i + half][32 * u + col];
+      s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qh[i], s, 0, 0, 0);
+      if constexpr (F32) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, ql[i], s, 0, 0, 0);
     }
-    if (j * 64 + 64 > lim_lo || r0 + 128 > rows) {
-      const int left = lim - j * 64 - 8 * half;  // result i of tile t is token 32 t + 16 (i / 8) + 8 half + i % 8
+  };
+  const auto second_product = [&](const u32x4 (&ph)[2], const u32x4 (&pl)[2], int buf, int u) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (32 * t + 16 * (i / 8) + i % 8 >= left) s16[t][i] = -INFINITY;
-    }
-    float top = -INFINITY;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, s16[t][i]);
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const float m_new = fmaxf(m_run, top * ck);
-    if (__any(m_new > m_run) || factor != 1.0f) {
-      const float alpha = exp2_fast(m_run - m_new);
-      l_run *= alpha;
-      const float f = alpha * factor;
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[d][i] *= f;
-      m_run = m_new;
-    }
-    const float off = kBias + (float)delta - m_run;
-    float sum = 0.0f;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      float p[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[i] = exp2_fast(fmaf(s16[s / 2][8 * (s % 2) + i], ck, off));
-        sum += p[i];
-      }
-      half8_t ph, pl;
-      to_half<F32>(p, ph, pl);
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
-        const half8_t vf = sv[buf][2 * s + half][32 * d + col];
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, ph, o[d], 0, 0, 0);
-        if constexpr (F32) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pl, o[d], 0, 0, 0);
+        const half8_t vf = sv[buf][4 * u + 2 * i + half][32 * d + col];
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, as_half8(ph[i]), o[d], 0, 0, 0);
+        if constexpr (F32) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, as_half8(pl[i]), o[d], 0, 0, 0);
       }
+  };
+  // Masks of scores s (half u of block j), where the block may reach past a row's tokens.
+  const auto mask = [&](f32x16& s, int j, int u) {
+    if (j * 64 + 32 * u + 32 > lim_lo) {
+      const int left = lim - j * 64 - 32 * u - 8 * half;  // result i is token 16 (i / 8) + 8 half + i % 8
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (16 * (i / 8) + i % 8 >= left) s[i] = -INFINITY;
     }
-    l_run = fmaf(sum, pow2f(-delta), l_run);
-    // the other buffer was last read before this iteration's barrier
-    if (j_n >= 0) stage(buf ^ 1, j_n);
-    buf ^= 1;
-    j = j_n;
-    block = block_n;
+  };
+  const auto rescale = [&](float f) {
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] *= f;
+  };
+  // After a step: probabilities in terms of an m that a row has left far behind do not
+  // fit f16. Their sum shows it (it is over kMost before any of them is over what f16
+  // holds), so no maximum is taken until then: m becomes the row's maximum, and the
+  // half's probabilities are computed again.
+  const auto settle = [&](const f32x16& s, u32x4 (&ph)[2], u32x4 (&pl)[2], float& sum, float ck, int delta) {
+    if (!__any(sum > kMost)) return;
+    float top = fmaxf(s[0], s[1]);
+#pragma unroll
+    for (int i = 2; i < 16; ++i) top = fmaxf(top, s[i]);
+    const float m_new = fmaxf(m_run, max_halves(top) * ck), alpha = exp2_fast(m_run - m_new);
+    l_run *= alpha;
+    m_run = m_new;
+    rescale(alpha);
+    const float off = kBias + (float)delta - m_run;
+    float p[16];
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i] = exp2_fast(fmaf(s[i], ck, off));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) take_p<F32>(p, i, sum, ph, pl);
+  };
+  // One half block: the softmax of scores s into ph, pl; the second product of the
+  // half before (qh_, ql_: its p; vbuf, vu: its V); the first product of the half
+  // after (into sn, from kbuf, ku); where `put` says so, the staging of the next
+  // block; and at the end, after `between`, the first reads of the next step (nbuf,
+  // nu). Written out in the order in which it is to run, one matrix instruction at
+  // a time with its share of the rest, and kept so: left to itself the compiler puts
+  // all matrix instructions first, each waiting for its own LDS read, and the softmax
+  // after them.
+  constexpr int SLOTS = 2 * NK, AHEAD = 4, PER = 16 / SLOTS;
+  half8_t first[AHEAD];  // operands of a step's first matrix instructions, read in the step before
+  const auto step = [&](const f32x16& s, u32x4 (&ph)[2], u32x4 (&pl)[2], const u32x4 (&oh)[2],
+                        const u32x4 (&ol)[2], int vbuf, int vu, f32x16& sn, int kbuf, int ku, float ck, int delta,
+                        float& sum, int nbuf, int nu, auto put, auto between) {
+    static_assert(NK == 2 * ND, "as many matrix instructions for the first product as for the second");
+    const auto operand = [&](int i) {
+      return i < NK ? sk[kbuf][2 * i + half][32 * ku + col]
+                    : sv[vbuf][4 * vu + 2 * ((i - NK) / ND) + half][32 * ((i - NK) % ND) + col];
+    };
+    const float off = kBias + (float)delta - m_run;
+    half8_t in[SLOTS];
+    float p[16];
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) in[i] = first[i];
+    sn = f32x16{};
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+      if (i + AHEAD < SLOTS) in[i + AHEAD] = operand(i + AHEAD);
+      if (i == SLOTS - 2) between();
+      if (i >= SLOTS - 2) {
+#pragma unroll
+        for (int k = 0; k < AHEAD / 2; ++k) {
+          const int n = (i - SLOTS + 2) * (AHEAD / 2) + k;
+          first[n] = sk[nbuf][2 * n + half][32 * nu + col];
+        }
+      }
+      // the first product first: its results are then there when the next step begins
+      if (i >= NK) {
+        const int k = i - NK;
+        o[k % ND] = __builtin_amdgcn_mfma_f32_32x32x16_f16(in[i], as_half8(oh[k / ND]), o[k % ND], 0, 0, 0);
+        if constexpr (F32) o[k % ND] = __builtin_amdgcn_mfma_f32_32x32x16_f16(in[i], as_half8(ol[k / ND]), o[k % ND], 0, 0, 0);
+      } else {
+        sn = __builtin_amdgcn_mfma_f32_32x32x16_f16(in[i], qh[i], sn, 0, 0, 0);
+        if constexpr (F32) sn = __builtin_amdgcn_mfma_f32_32x32x16_f16(in[i], ql[i], sn, 0, 0, 0);
+      }
+#pragma unroll
+      for (int e = i * PER; e < (i + 1) * PER; ++e) p[e] = exp2_fast(fmaf(s[e], ck, off));
+      if (i > 0) {
+#pragma unroll
+        for (int e = (i - 1) * PER; e < i * PER; ++e) take_p<F32>(p, e, sum, ph, pl);
+      }
+      if (i < SLOTS - 2) put(i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int e = 16 - PER; e < 16; ++e) take_p<F32>(p, e, sum, ph, pl);
+  };
+
+  Walk walk(g, list, b, h, from, to, lane);
+  int block = -1, block1 = -1, block2 = -1, ev = 0, ev1 = 0, ev2 = 0;
+  float ks = 0.0f, ks1 = 0.0f, ks2 = 0.0f;
+  int j = walk.next(block, ks, ev);
+  if (j >= 0) {
+    f32x16 sa, sb;
+    u32x4 pa[2] = {}, pb[2] = {}, la[2] = {}, lb[2] = {};
+    // past the last block the registers are loaded with it again (not used), so that
+    // the steps have no branch
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+      load_k(block, u);
+      load_v(block, u);
+    }
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+      put_k(0, u, 0);
+      put_k(0, u, 1);
+    }
+    for (int i = tid; i < 8 * D; i += 256) sv[1][0][i] = half8_t{};  // the pending product of the first half: zero
+    block1 = block;
+    int j1 = walk.next(block1, ks1, ev1), buf = 0;
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) load_k(block1, u);
+    __syncthreads();
+    first_product(sa, 0, 0);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) first[i] = sk[0][2 * i + half][32 + col];
+    while (true) {
+      const float ck = cq * ks;
+      float factor, sum;
+      const int delta = enter_block(ev_cur, ev, factor);
+      const float back = pow2f(-delta);
+      if (j * 64 + 64 > len) {
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) vr[u] = keep_codes(vr[u], len - j * 64 - 16 * ((tid + 256 * u) / D));
+      }
+      // half 2 t. The buffers written here were last read before the previous block's
+      // barrier. A register's next load follows its last use: a whole block ahead.
+      block2 = block1;
+      const int j2 = j1 >= 0 ? walk.next(block2, ks2, ev2) : -1;
+      mask(sa, j, 0);
+      step(sa, pa, la, pb, lb, buf ^ 1, 1, sb, buf, 1, ck, delta, sum, buf ^ 1, 0, [&](int i) {
+        // half a unit in each of 4 * UNITS slots: V, then K
+        constexpr int FROM = 1;
+        static_assert(FROM + 4 * UNITS <= SLOTS - 2 || UNITS == 0, "staged before the barrier");
+        const int k = i - FROM, u = k / 2 % UNITS;
+        if (k < 0 || k >= 4 * UNITS) return;
+        if (k < 2 * UNITS) {
+          put_v(buf, u, k % 2);
+          if (k % 2) load_v(block1, u);
+        } else {
+          put_k(buf ^ 1, u, k % 2);
+          if (k % 2) load_k(block2, u);
+        }
+      }, [] { __syncthreads(); });
+      if (factor != 1.0f) rescale(factor);
+      settle(sa, pa, la, sum, ck, delta);
+      l_run = fmaf(sum, back, l_run);
+      // half 2 t + 1
+      mask(sb, j, 1);
+      step(sb, pb, lb, pa, la, buf, 0, sa, buf ^ 1, 0, ck, delta, sum, buf ^ 1, 1, [](int) {}, [] {});
+      settle(sb, pb, lb, sum, ck, delta);
+      l_run = fmaf(sum, back, l_run);
+      if (j1 < 0) break;
+      buf ^= 1;
+      j = j1; block = block1; ks = ks1; ev = ev1;
+      j1 = j2; block1 = block2; ks1 = ks2; ev1 = ev2;
+    }
+    second_product(pb, lb, buf, 1);
   }
   l_run += __shfl_xor(l_run, 32);
   if (!live) return;
@@ -553,8 +756,9 @@ hipError_t run(const KvAttendArgs& a, bool few, hipStream_t s) {
     const dim3 grid((unsigned)(a.splits * groups), (unsigned)a.g.kv_heads, (unsigned)a.g.batch);
     kv_attend_few_kernel<D, F32><<<grid, 256, 0, s>>>(a);
   } else {
-    const dim3 grid((unsigned)(a.splits * ((rows + 127) / 128)), (unsigned)a.g.kv_heads, (unsigned)a.g.batch);
-    kv_attend_many_kernel<D, F32><<<grid, 256, 0, s>>>(a);
+    const int64_t grid = a.splits * ((rows + 127) / 128) * a.g.kv_heads * a.g.batch;
+    if (grid > INT32_MAX) return hipErrorInvalidValue;
+    kv_attend_many_kernel<D, F32><<<(unsigned)grid, 256, 0, s>>>(a);
   }
   hipError_t err = hipGetLastError();
   if (err == hipSuccess && a.splits > 1) {

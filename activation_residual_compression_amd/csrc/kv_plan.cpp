@@ -40,7 +40,7 @@ Way way_of(const rc_kv_plan* pl, int64_t queries, int64_t blocks, bool chosen) {
     splits = std::min(ceil_div(1024, base), ceil_div(blocks, 4));
   } else {
     const int64_t base = heads * ceil_div(rows, 128);
-    if (base < 384) splits = std::min(ceil_div(512, base), ceil_div(blocks, 8));
+    if (base < 192) splits = std::min(std::max<int64_t>(256 / base, 1), ceil_div(blocks, 8));
   }
   w.splits = (int)std::max<int64_t>(splits, 1);
   w.part_rows = w.splits > 1 ? w.splits * heads * rows : 0;
