@@ -52,11 +52,15 @@ struct KvAttendArgs {
   int queries, causal;
   int q_tile, keep, tiles;
   float scale;            // of the scores
-  // partial results of a split over the keys: [split][batch * kv_heads * rows][D],
-  // then (m, l) pairs; null with one split
-  int splits;
+  // Split over the keys: a group of rows that reads n blocks does so in
+  // ceil(n / chunk) parts of equal length, at most `splits`, each by a block of
+  // threads of its own. With one part it writes the outputs; with more, each writes
+  // partial results [part][batch * kv_heads * rows][D] and (m, l), which are joined.
+  int splits, chunk;
   float* part;
   float2* part_ml;
+  int32_t* part_n;   // kernel for many rows: parts of each row, for the launch that joins them
+  uint32_t* arrived; // kernel for few rows: parts done of each group, 0 between calls; the last one joins them
 };
 hipError_t launch_kv_select(const KvAttendArgs& a, bool bf16, hipStream_t s);
 // few: the kernel for few rows (16 rows of a key head per block), else the one

@@ -108,6 +108,15 @@ __device__ __forceinline__ void take_p(const float (&p)[16], int e, float& sum, 
 }
 __device__ __forceinline__ half8_t as_half8(u32x4 x) { return __builtin_bit_cast(half8_t, x); }
 
+// The part of a group's n blocks that this block of threads reads; parts: of how many.
+__device__ __forceinline__ bool part_of(const KvAttendArgs& a, int n, int split, int& parts, int& from, int& to) {
+  parts = min(max((n + a.chunk - 1) / a.chunk, 1), a.splits);
+  const int per = (n + parts - 1) / parts;
+  from = split * per;
+  to = min(from + per, n);
+  return split < parts;
+}
+
 // Keeps the first n of the 16 codes of u (n <= 0: none), so that stale codes after
 // a sequence's end never meet a probability of zero as a NaN.
 __device__ __forceinline__ u32x4 keep_codes(u32x4 u, int n) {
@@ -120,17 +129,86 @@ __device__ __forceinline__ u32x4 keep_codes(u32x4 u, int n) {
   return u;
 }
 
+// Two floats written to, read from, memory that every XCD sees.
+__device__ __forceinline__ void put_pair(float* p, float2 x) {
+  const uint64_t u = (uint64_t)__float_as_uint(x.y) << 32 | __float_as_uint(x.x);
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 get_pair(const float* p) {
+  const uint64_t u = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__uint_as_float((uint32_t)u), __uint_as_float((uint32_t)(u >> 32)));
+}
+
+// The blocks that a wave reads, entries from, from + step, ... below to, one after the
+// other, without a load in the way: the wave's 64 lanes hold the next 64 (index, pool
+// block, scales), loaded at once, and hand them out one by one. Blocks that do not
+// exist are skipped.
+struct Walk {
+  const KvGeom& g;
+  const int32_t* list;
+  int b, h, base, to, step, lane;
+  uint64_t left;  // entries of these 64 still to come
+  int lane_j, lane_block;
+  float lane_ks, lane_vs;
+
+  __device__ __forceinline__ Walk(const KvGeom& g, const int32_t* list, int b, int h, int from, int to, int step,
+                                  int lane)
+      : g(g), list(list), b(b), h(h), base(from - 64 * step), to(to), step(step), lane(lane), left(0) {}
+  __device__ __forceinline__ void fill() {
+    base += 64 * step;
+    lane_block = -1;
+    const int at = base + lane * step;
+    if (at < to) {
+      lane_j = list ? list[at] : at;
+      lane_block = kv_block(g, b, lane_j);
+    }
+    if (lane_block >= 0) {
+      lane_ks = g.k_scale[kv_row(g, lane_block, h)];
+      lane_vs = g.v_scale[kv_row(g, lane_block, h)];
+    }
+    left = __ballot(lane_block >= 0);
+  }
+  // Moves to the next block: its index (-1: none) and pool block; `at` is its lane.
+  __device__ __forceinline__ int next(int& block, int& at) {
+    while (left == 0) {
+      if (base + 64 * step >= to) return -1;
+      fill();
+    }
+    at = __builtin_ctzll(left);
+    left &= left - 1;
+    block = __builtin_amdgcn_readlane(lane_block, at);
+    return __builtin_amdgcn_readlane(lane_j, at);
+  }
+  // Scales of the block that next() found, before the next call of it.
+  __device__ __forceinline__ float k_scale(int at) const {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(lane_ks), at));
+  }
+  __device__ __forceinline__ int v_exponent(int at) const {
+    return scale_exponent(__uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(lane_vs), at)));
+  }
+  __device__ __forceinline__ int next(int& block, float& ks, int& ev) {
+    int at;
+    const int j = next(block, at);
+    if (j >= 0) {
+      ks = k_scale(at);
+      ev = v_exponent(at);
+    }
+    return j;
+  }
+};
+
 // ------------------------------------------------------------------ few rows
 // One block of threads: 16 rows of one key head, a part of the keys. Each of its
 // four waves reads blocks of its own straight into registers (a block's K and V
 // are 16 loads of 16 B a lane) and keeps its own running maximum and sum; the four
-// are joined in LDS. HBM bound: every code is read once for 16 rows.
+// are joined in LDS, and the parts of the keys by the one that is done last. HBM bound: every code is read once for 16 rows.
 template <int D, bool F32>
 __global__ __launch_bounds__(256, 2) void kv_attend_few_kernel(KvAttendArgs a) {
   constexpr int ND = D / 16, NQ = D / 64;
   typedef typename std::conditional<F32, float, uint16_t>::type IO;
   __shared__ float so[4][16][D + 4];
   __shared__ float2 sml[4][16];
+  __shared__ bool last;
   const KvGeom& g = a.g;
   // groups of 16 rows do not cross what shares a list of blocks: with q_tile 1 a query's rows (span)
   const int rows = a.queries * g.group, span = a.blocks && a.q_tile == 1 ? g.group : rows;
@@ -153,8 +231,8 @@ __global__ __launch_bounds__(256, 2) void kv_attend_few_kernel(KvAttendArgs a) {
     list = a.blocks + (((int64_t)b * g.kv_heads + h) * a.tiles + tile) * a.keep;
     count = list_length(list, a.keep, reach, lane);
   }
-  const int per = (count + a.splits - 1) / a.splits;
-  const int from = split * per, to = min(from + per, count);
+  int parts, from, to;
+  if (!part_of(a, count, split, parts, from, to)) return;
 
   half8_t qh[NQ][2], ql[NQ][2];
   float cq;
@@ -190,10 +268,9 @@ __global__ __launch_bounds__(256, 2) void kv_attend_few_kernel(KvAttendArgs a) {
   for (int d = 0; d < ND; ++d) o[d] = f32x4{0, 0, 0, 0};
   float m_run = kLowest, l_run = 0.0f;
   int ev_cur = 0;
-  for (int it = from + wave; it < to; it += 4) {
-    const int j = list ? list[it] : it;
-    const int block = kv_block(g, b, j);
-    if (block < 0) continue;
+  Walk walk(g, list, b, h, from + wave, to, 4, lane);
+  int block, slot;
+  for (int j; (j = walk.next(block, slot)) >= 0;) {
     const int64_t row = kv_row(g, block, h);
     const uint8_t* kb = g.k + row * (64 * D);
     const uint8_t* vb = g.v + row * (64 * D);
@@ -205,9 +282,9 @@ __global__ __launch_bounds__(256, 2) void kv_attend_few_kernel(KvAttendArgs a) {
         k[t][s] = *reinterpret_cast<const u32x4*>(kb + ((4 * s + quad) * 64 + 16 * (col >> 2) + 4 * t + (col & 3)) * 16);
 #pragma unroll
     for (int d = 0; d < ND; ++d) v[d] = *reinterpret_cast<const u32x4*>(vb + (quad * D + 16 * d + col) * 16);
-    const float ck = cq * g.k_scale[row];
+    const float ck = cq * walk.k_scale(slot);
     float factor;
-    const int delta = enter_block(ev_cur, scale_exponent(g.v_scale[row]), factor);
+    const int delta = enter_block(ev_cur, walk.v_exponent(slot), factor);
 
     f32x4 s4[4];
 #pragma unroll
@@ -284,7 +361,7 @@ __global__ __launch_bounds__(256, 2) void kv_attend_few_kernel(KvAttendArgs a) {
 
   // join the waves: 16 threads a row, D / 16 values each
   const int rr = tid >> 4, d0 = (tid & 15) * ND;
-  if (r0 + rr >= r1) return;
+  const bool mine = r0 + rr < r1;
   float m = kLowest, l = 0.0f, f[4];
 #pragma unroll
   for (int w = 0; w < 4; ++w) m = fmaxf(m, sml[w][rr].x);
@@ -293,27 +370,65 @@ __global__ __launch_bounds__(256, 2) void kv_attend_few_kernel(KvAttendArgs a) {
     f[w] = exp2_fast(sml[w][rr].x - m);
     l += sml[w][rr].y * f[w];
   }
-  float x[ND];
+  f32x4 x[ND / 4];
 #pragma unroll
-  for (int i = 0; i < ND; ++i) {
-    x[i] = 0.0f;
+  for (int i = 0; i < ND / 4; ++i) {
+    x[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < 4; ++w) x[i] += so[w][rr][d0 + i] * f[w];
+    for (int w = 0; w < 4; ++w) x[i] += *reinterpret_cast<const f32x4*>(&so[w][rr][d0 + 4 * i]) * f[w];
   }
-  if (a.splits > 1) {
-    const int64_t at = ((int64_t)split * g.batch + b) * g.kv_heads * rows + (int64_t)h * rows + r0 + rr;
+  if (parts > 1) {
+    // The part that is done last joins them all, in their order, so the result does not
+    // depend on which one that was. Partial results pass between XCDs, whose L2 caches
+    // are not coherent: they are written and read past them (put_pair, get_pair). A
+    // fence instead would write back the whole L2 for every block of threads (measured:
+    // 368 us for a call that takes 65).
+    const int64_t all = (int64_t)g.batch * g.kv_heads * rows, at = ((int64_t)b * g.kv_heads + h) * rows + r0 + rr;
+    if (mine) {
 #pragma unroll
-    for (int i = 0; i < ND; ++i) a.part[at * D + d0 + i] = x[i];
-    if ((tid & 15) == 0) a.part_ml[at] = make_float2(m, l);
-    return;
+      for (int i = 0; i < ND / 4; ++i) {
+        put_pair(a.part + (split * all + at) * D + d0 + 4 * i, make_float2(x[i].x, x[i].y));
+        put_pair(a.part + (split * all + at) * D + d0 + 4 * i + 2, make_float2(x[i].z, x[i].w));
+      }
+      if ((tid & 15) == 0) put_pair(&a.part_ml[split * all + at].x, make_float2(m, l));
+    }
+    uint32_t* arrived = a.arrived + ((int64_t)b * g.kv_heads + h) * (gridDim.x / a.splits) + group;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this thread's stores are done
+    __syncthreads();
+    if (tid == 0) last = atomicAdd(arrived, 1u) == (uint32_t)parts - 1u;
+    __syncthreads();
+    if (!last) return;
+    if (tid == 0) *arrived = 0;
+    if (!mine) return;
+    m = kLowest;
+    l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < ND / 4; ++i) x[i] = f32x4{0, 0, 0, 0};
+#pragma unroll 2
+    for (int s = 0; s < parts; ++s) {
+      const float2 ml = get_pair(&a.part_ml[s * all + at].x);
+      float2 y[ND / 2];
+#pragma unroll
+      for (int i = 0; i < ND / 2; ++i) y[i] = get_pair(a.part + (s * all + at) * D + d0 + 2 * i);
+      const float m_new = fmaxf(m, ml.x), fo = exp2_fast(m - m_new), fs = exp2_fast(ml.x - m_new);
+      m = m_new;
+      l = l * fo + ml.y * fs;
+#pragma unroll
+      for (int i = 0; i < ND / 4; ++i)
+        x[i] = x[i] * fo + f32x4{y[2 * i].x, y[2 * i].y, y[2 * i + 1].x, y[2 * i + 1].y} * fs;
+    }
   }
+  if (!mine) return;
   const Row to_row = row_of(a, h, r0 + rr);
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
   IO* out = (IO*)a.out.data + b * a.out.sb + (int64_t)to_row.query * a.out.st + to_row.head * a.out.sh + d0;
 #pragma unroll
-  for (int i = 0; i < ND; ++i) {
-    if constexpr (F32) out[i] = x[i] * inv;
-    else out[i] = (uint16_t)bf16_rne(x[i] * inv);
+  for (int i = 0; i < ND / 4; ++i) {
+    const f32x4 y = x[i] * inv;
+    if constexpr (F32)
+      *reinterpret_cast<f32x4*>(out + 4 * i) = y;
+    else
+      *reinterpret_cast<u32x2*>(out + 4 * i) = u32x2{bf16_rne(y.x) | bf16_rne(y.y) << 16, bf16_rne(y.z) | bf16_rne(y.w) << 16};
   }
   if (a.lse && (tid & 15) == 0)
     a.lse[((int64_t)b * a.queries + to_row.query) * g.q_heads + to_row.head] =
@@ -321,47 +436,6 @@ __global__ __launch_bounds__(256, 2) void kv_attend_few_kernel(KvAttendArgs a) {
 }
 
 // ------------------------------------------------------------------ many rows
-// The blocks that a part of a call reads, one after the other, without a load in
-// the way: the wave's 64 lanes hold the next 64 entries (index, pool block, scales),
-// loaded at once, and hand them out one by one. Blocks that do not exist are skipped.
-struct Walk {
-  const KvGeom& g;
-  const int32_t* list;
-  int b, h, base, to, lane;
-  uint64_t left;  // entries of this 64 still to come
-  int lane_j, lane_block;
-  float lane_ks, lane_vs;
-
-  __device__ __forceinline__ Walk(const KvGeom& g, const int32_t* list, int b, int h, int from, int to, int lane)
-      : g(g), list(list), b(b), h(h), base(from - 64), to(to), lane(lane), left(0) {}
-  __device__ __forceinline__ void fill() {
-    base += 64;
-    lane_block = -1;
-    if (base + lane < to) {
-      lane_j = list ? list[base + lane] : base + lane;
-      lane_block = kv_block(g, b, lane_j);
-      if (lane_block >= 0) {
-        lane_ks = g.k_scale[kv_row(g, lane_block, h)];
-        lane_vs = g.v_scale[kv_row(g, lane_block, h)];
-      }
-    }
-    left = __ballot(lane_block >= 0);
-  }
-  // The next block: its index j (-1: none), pool block and scales.
-  __device__ __forceinline__ int next(int& block, float& ks, int& ev) {
-    while (left == 0) {
-      if (base + 64 >= to) return -1;
-      fill();
-    }
-    const int i = __builtin_ctzll(left);
-    left &= left - 1;
-    block = __builtin_amdgcn_readlane(lane_block, i);
-    ks = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(lane_ks), i));
-    ev = scale_exponent(__uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(lane_vs), i)));
-    return __builtin_amdgcn_readlane(lane_j, i);
-  }
-};
-
 // Which part of the call a block of threads does. They go to the 8 XCDs in turn, so
 // where the load of the XCDs stays even, a key head's row tiles are given to one XCD,
 // whose L2 then holds its K and V: with a multiple of 8 key heads, head h to XCD h % 8
@@ -391,8 +465,8 @@ __device__ __forceinline__ Place place_of(const KvAttendArgs& a, uint32_t w, uin
     b = 0;
   } else {
     const uint32_t all = heads * (uint32_t)a.g.batch;
-    in_head = w / (all * a.splits) * a.splits + w % (uint32_t)a.splits;
-    w = w / a.splits % all;
+    in_head = w / all;
+    w %= all;
     h = w % heads;
     b = w / heads;
   }
@@ -442,8 +516,8 @@ __global__ __launch_bounds__(256, D == 128 && F32 ? 1 : 2) void kv_attend_many_k
     list = a.blocks + (((int64_t)b * g.kv_heads + h) * a.tiles + (r0 / g.group) / a.q_tile) * a.keep;
     count = list_length(list, a.keep, reach, lane);
   }
-  const int per = (count + a.splits - 1) / a.splits;
-  const int from = split * per, to = min(from + per, count);
+  int parts, from, to;
+  if (!part_of(a, count, split, parts, from, to)) return;
 
   half8_t qh[NK], ql[NK];
   float cq;
@@ -609,7 +683,7 @@ __global__ __launch_bounds__(256, D == 128 && F32 ? 1 : 2) void kv_attend_many_k
     for (int e = 16 - PER; e < 16; ++e) take_p<F32>(p, e, sum, ph, pl);
   };
 
-  Walk walk(g, list, b, h, from, to, lane);
+  Walk walk(g, list, b, h, from, to, 1, lane);
   int block = -1, block1 = -1, block2 = -1, ev = 0, ev1 = 0, ev2 = 0;
   float ks = 0.0f, ks1 = 0.0f, ks2 = 0.0f;
   int j = walk.next(block, ks, ev);
@@ -683,7 +757,8 @@ __global__ __launch_bounds__(256, D == 128 && F32 ? 1 : 2) void kv_attend_many_k
   l_run += __shfl_xor(l_run, 32);
   if (!live) return;
   const float unit = pow2f(ev_cur);
-  if (a.splits > 1) {
+  if (a.splits > 1 && split == 0 && half == 0) a.part_n[((int64_t)b * g.kv_heads + h) * rows + r] = parts;
+  if (parts > 1) {
     const int64_t at = ((int64_t)split * g.batch + b) * g.kv_heads * rows + (int64_t)h * rows + r;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
@@ -713,37 +788,38 @@ __global__ __launch_bounds__(256, D == 128 && F32 ? 1 : 2) void kv_attend_many_k
 }
 
 // ------------------------------------------------------------------ joining splits
-// One wave a row: out = sum O_s 2^(m_s - m) / sum l_s 2^(m_s - m).
+// D / 4 lanes a row: out = sum O_s 2^(m_s - m) / sum l_s 2^(m_s - m), parts in order.
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void kv_attend_join_kernel(KvAttendArgs a) {
   typedef typename std::conditional<F32, float, uint16_t>::type IO;
-  constexpr int W = D / 64;
+  constexpr int LANES = D / 4;
   const KvGeom& g = a.g;
   const int64_t rows = (int64_t)a.queries * g.group, all = rows * g.kv_heads * g.batch;
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
+  const int64_t at = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  const int d0 = threadIdx.x % LANES * 4;
   if (at >= all) return;
-  float m = kLowest, l = 0.0f, x[W];
-#pragma unroll
-  for (int i = 0; i < W; ++i) x[i] = 0.0f;
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.part_ml[s * all + at].x);
-  for (int s = 0; s < a.splits; ++s) {
+  const int parts = a.part_n[at];
+  if (parts == 1) return;
+  float m = kLowest, l = 0.0f;
+  f32x4 x = {0, 0, 0, 0};
+  for (int s = 0; s < parts; ++s) m = fmaxf(m, a.part_ml[s * all + at].x);
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s) {
     const float2 ml = a.part_ml[s * all + at];
+    const f32x4 o = *reinterpret_cast<const f32x4*>(a.part + (s * all + at) * D + d0);
     const float f = exp2_fast(ml.x - m);
     l += ml.y * f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) x[i] += a.part[(s * all + at) * D + lane * W + i] * f;
+    x += o * f;
   }
   const int r = (int)(at % rows), h = (int)(at / rows % g.kv_heads), b = (int)(at / rows / g.kv_heads);
   const Row me = row_of(a, h, r);
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  IO* out = (IO*)a.out.data + b * a.out.sb + (int64_t)me.query * a.out.st + me.head * a.out.sh + lane * W;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    if constexpr (F32) out[i] = x[i] * inv;
-    else out[i] = (uint16_t)bf16_rne(x[i] * inv);
-  }
-  if (a.lse && lane == 0)
+  x *= l > 0.0f ? 1.0f / l : 0.0f;
+  IO* out = (IO*)a.out.data + b * a.out.sb + (int64_t)me.query * a.out.st + me.head * a.out.sh + d0;
+  if constexpr (F32)
+    *reinterpret_cast<f32x4*>(out) = x;
+  else
+    *reinterpret_cast<u32x2*>(out) = u32x2{bf16_rne(x.x) | bf16_rne(x.y) << 16, bf16_rne(x.z) | bf16_rne(x.w) << 16};
+  if (a.lse && d0 == 0)
     a.lse[((int64_t)b * a.queries + me.query) * g.q_heads + me.head] =
         l > 0.0f ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
 }
@@ -761,8 +837,9 @@ hipError_t run(const KvAttendArgs& a, bool few, hipStream_t s) {
     kv_attend_many_kernel<D, F32><<<(unsigned)grid, 256, 0, s>>>(a);
   }
   hipError_t err = hipGetLastError();
-  if (err == hipSuccess && a.splits > 1) {
-    kv_attend_join_kernel<D, F32><<<(unsigned)((rows * a.g.kv_heads * a.g.batch + 3) / 4), 256, 0, s>>>(a);
+  if (err == hipSuccess && a.splits > 1 && !few) {
+    const int64_t per = 256 / (D / 4);
+    kv_attend_join_kernel<D, F32><<<(unsigned)((rows * a.g.kv_heads * a.g.batch + per - 1) / per), 256, 0, s>>>(a);
     err = hipGetLastError();
   }
   return err;

@@ -12,22 +12,30 @@ struct rc_kv_plan {
   rc_kv_shape_t shape;
   rc_dtype_t dtype;
   rc_kv_params_t params;
-  void* ws = nullptr;  // partial outputs of a split, then their (m, l)
+  void* ws = nullptr;  // partial results: outputs, (m, l), numbers of parts
   size_t ws_bytes = 0;
+  int64_t part_rows = 0;  // rows of partial results that it holds
+  uint32_t* arrived = nullptr;  // [kFewBlocks], after them
 };
 
 namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// How a call runs: which kernel, over how many parts of the keys.
+// Blocks of threads that the kernel for few rows is split into, where there are
+// fewer groups of rows: two for each that the CUs hold at once (three), so that the
+// ragged ends of sequences even out.
+constexpr int64_t kFewBlocks = 1536;
+
+// How a call runs: which kernel, and in how many parts of which length a group of
+// rows reads its blocks.
 struct Way {
   bool few;
-  int splits;
-  int64_t part_rows;  // rows of partial results; 0 with one split
+  int splits, chunk;
+  int64_t part_rows;  // rows of partial results; 0 with one part
 };
 
-Way way_of(const rc_kv_plan* pl, int64_t queries, int64_t blocks, bool chosen) {
+Way way_of(const rc_kv_plan* pl, int64_t queries, int64_t blocks, bool chosen, int64_t most_rows) {
   const rc_kv_shape_t& s = pl->shape;
   const int64_t group = s.q_heads / s.kv_heads, rows = queries * group;
   const bool own_lists = chosen && pl->params.q_tile == 1;
@@ -35,20 +43,57 @@ Way way_of(const rc_kv_plan* pl, int64_t queries, int64_t blocks, bool chosen) {
   w.few = own_lists || rows <= 64;
   const int64_t heads = (int64_t)s.batch * s.kv_heads;
   int64_t splits = 1;
+  blocks = std::max<int64_t>(blocks, 1);
   if (w.few) {
     const int64_t base = heads * (own_lists ? queries * ceil_div(group, 16) : ceil_div(rows, 16));
-    splits = std::min(ceil_div(1024, base), ceil_div(blocks, 4));
+    splits = std::min({ceil_div(kFewBlocks, base), ceil_div(blocks, 4), most_rows / (heads * rows)});
   } else {
+    // Blocks of threads that a CU holds at once (registers and LDS of the kernel).
+    const bool f32 = pl->dtype == RC_F32;
+    const int64_t at_once = 256 * (s.head_dim == 128 ? (f32 ? 1 : 2) : (f32 ? 2 : 3));
     const int64_t base = heads * ceil_div(rows, 128);
-    if (base < 192) splits = std::min(std::max<int64_t>(256 / base, 1), ceil_div(blocks, 8));
+    // The time in steps of one block (about 1.8 us where the CUs are full): whole
+    // rounds of equal parts, or for causal rows, whose parts differ and are started
+    // longest first, the average and half the longest. Partial results cost a write
+    // and a read, and the launch that joins them.
+    const bool causal = (pl->params.flags & RC_KV_CAUSAL) && !chosen;
+    double best = 0.0;
+    for (int64_t p = 1; p <= std::min({(int64_t)16, ceil_div(blocks, 8), std::max<int64_t>(most_rows / (heads * rows), 1)});
+         ++p) {
+      const double len = (double)ceil_div(blocks, p);
+      const double mean = std::max(1.0, (double)blocks - (causal ? (double)std::min(queries / 128, blocks / 2) : 0.0));
+      double cost = causal ? std::max((double)base * mean / at_once, len) + 0.5 * len
+                           : (double)ceil_div(base * p, at_once) * len;
+      if (p > 1) cost += 3.0 + (double)(heads * rows * p) * (8.0 * s.head_dim) / 4e6 / 1.8;
+      if (p == 1 || cost < best) {
+        best = cost;
+        splits = p;
+      }
+    }
   }
   w.splits = (int)std::max<int64_t>(splits, 1);
+  w.chunk = (int)ceil_div(blocks, w.splits);
   w.part_rows = w.splits > 1 ? w.splits * heads * rows : 0;
   return w;
 }
 
 size_t part_bytes(const rc_kv_plan* pl, int64_t part_rows) {
-  return (size_t)part_rows * ((size_t)pl->shape.head_dim * 4 + sizeof(float2));
+  // outputs, (m, l), and the number of parts (a row of the first part)
+  return (size_t)part_rows * ((size_t)pl->shape.head_dim * 4 + sizeof(float2) + sizeof(int32_t));
+}
+
+// Rows that the workspace is made for: what whole sequences need for the largest
+// number of queries and for smaller ones, at most half a gigabyte. A call that would
+// need more takes fewer parts.
+int64_t part_rows_at_most(const rc_kv_plan* pl) {
+  const int64_t cap = ((int64_t)512 << 20) / (int64_t)part_bytes(pl, 1);
+  int64_t most = 0, q = pl->params.max_queries;
+  while (true) {
+    most = std::max(most, way_of(pl, q, pl->shape.seq_blocks, false, cap).part_rows);
+    if (pl->params.q_tile) most = std::max(most, way_of(pl, q, pl->params.keep_blocks, true, cap).part_rows);
+    if (q == 1) return most;
+    q = q > 64 ? std::max<int64_t>(q / 2, 64) : q - 1;
+  }
 }
 
 rc_status_t check(const rc_kv_shape_t& s, rc_dtype_t dtype, const rc_kv_params_t* p) {
@@ -144,7 +189,10 @@ rc_status_t prepare(rc_kv_plan* pl, const rc_kv_cache_t* cache, const int32_t* t
   a->blocks = nullptr;
   a->blocks_out = nullptr;
   a->splits = 1;
+  a->chunk = 1;
   a->part = nullptr;
+  a->part_n = nullptr;
+  a->arrived = nullptr;
   a->part_ml = nullptr;
   a->out = {nullptr, 0, 0, 0};
   return RC_OK;
@@ -165,18 +213,20 @@ rc_status_t rc_kv_plan_create(rc_kv_shape_t shape, rc_dtype_t dtype, const rc_kv
   pl->shape = shape;
   pl->dtype = dtype;
   pl->params = *params;
-  // the most that any number of queries needs (fewer blocks mean fewer splits);
-  // more queries than this are never split
-  int64_t most = 0;
-  const int64_t top = std::min<int64_t>(params->max_queries, 65536);
-  for (int64_t q = 1; q <= top; ++q) {
-    most = std::max(most, way_of(pl, q, shape.seq_blocks, false).part_rows);
-    if (params->q_tile) most = std::max(most, way_of(pl, q, params->keep_blocks, true).part_rows);
-  }
-  pl->ws_bytes = part_bytes(pl, most);
-  if (pl->ws_bytes && hipMalloc(&pl->ws, pl->ws_bytes) != hipSuccess) {
-    delete pl;
-    return RC_ERR_HIP;
+  pl->part_rows = part_rows_at_most(pl);
+  if (pl->part_rows) {
+    const size_t parts = part_bytes(pl, pl->part_rows), counts = kFewBlocks * sizeof(uint32_t);
+    if (hipMalloc(&pl->ws, parts + counts) != hipSuccess) {
+      delete pl;
+      return RC_ERR_HIP;
+    }
+    pl->ws_bytes = parts + counts;
+    pl->arrived = reinterpret_cast<uint32_t*>(static_cast<char*>(pl->ws) + parts);
+    if (hipMemset(pl->arrived, 0, counts) != hipSuccess) {
+      (void)hipFree(pl->ws);
+      delete pl;
+      return RC_ERR_HIP;
+    }
   }
   *out = pl;
   return RC_OK;
@@ -231,12 +281,14 @@ rc_status_t rc_kv_attend(rc_kv_plan_t pl, hipStream_t stream, const rc_kv_cache_
   a.blocks = blocks;
   int64_t reach = ceil_div(a.max_len, RC_KV_BLOCK);
   if (blocks) reach = std::min<int64_t>(reach, a.keep);
-  const Way w = way_of(pl, queries, reach, blocks != nullptr);
+  const Way w = way_of(pl, queries, reach, blocks != nullptr, pl->part_rows);
   a.splits = w.splits;
+  a.chunk = w.chunk;
   if (w.splits > 1) {
-    if (part_bytes(pl, w.part_rows) > pl->ws_bytes) return RC_ERR_INVALID_ARG;  // not reached: sized for it
     a.part = static_cast<float*>(pl->ws);
     a.part_ml = reinterpret_cast<float2*>(a.part + w.part_rows * s.head_dim);
+    a.part_n = reinterpret_cast<int32_t*>(a.part_ml + w.part_rows);
+    a.arrived = pl->arrived;
   }
   return rc::launch_kv_attend(a, w.few, pl->dtype == RC_BF16, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
 }
