@@ -148,8 +148,7 @@ struct Walk {
   const int32_t* list;
   int b, h, base, to, step, lane;
   uint64_t left;  // entries of these 64 still to come
-  int lane_j, lane_block;
-  float lane_ks, lane_vs;
+  int lane_j, lane_block, lane_e;  // lane_e: the exponents of K's and V's scales, 16 bits each
 
   __device__ __forceinline__ Walk(const KvGeom& g, const int32_t* list, int b, int h, int from, int to, int step,
                                   int lane)
@@ -163,8 +162,8 @@ struct Walk {
       lane_block = kv_block(g, b, lane_j);
     }
     if (lane_block >= 0) {
-      lane_ks = g.k_scale[kv_row(g, lane_block, h)];
-      lane_vs = g.v_scale[kv_row(g, lane_block, h)];
+      const int64_t row = kv_row(g, lane_block, h);
+      lane_e = scale_exponent(g.k_scale[row]) << 16 | (scale_exponent(g.v_scale[row]) & 0xFFFF);
     }
     left = __ballot(lane_block >= 0);
   }
@@ -179,20 +178,16 @@ struct Walk {
     block = __builtin_amdgcn_readlane(lane_block, at);
     return __builtin_amdgcn_readlane(lane_j, at);
   }
-  // Scales of the block that next() found, before the next call of it.
-  __device__ __forceinline__ float k_scale(int at) const {
-    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(lane_ks), at));
-  }
-  __device__ __forceinline__ int v_exponent(int at) const {
-    return scale_exponent(__uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(lane_vs), at)));
+  // Exponents of the scales of the block that next() found, before the next call of it.
+  __device__ __forceinline__ void scales(int at, float& ks, int& ev) const {
+    const int e = __builtin_amdgcn_readlane(lane_e, at);
+    ks = pow2f(e >> 16);
+    ev = (int16_t)e;
   }
   __device__ __forceinline__ int next(int& block, float& ks, int& ev) {
     int at;
     const int j = next(block, at);
-    if (j >= 0) {
-      ks = k_scale(at);
-      ev = v_exponent(at);
-    }
+    if (j >= 0) scales(at, ks, ev);
     return j;
   }
 };
@@ -203,7 +198,7 @@ struct Walk {
 // are 16 loads of 16 B a lane) and keeps its own running maximum and sum; the four
 // are joined in LDS, and the parts of the keys by the one that is done last. HBM bound: every code is read once for 16 rows.
 template <int D, bool F32>
-__global__ __launch_bounds__(256, 2) void kv_attend_few_kernel(KvAttendArgs a) {
+__global__ __launch_bounds__(256, F32 ? 2 : 3) void kv_attend_few_kernel(KvAttendArgs a) {
   constexpr int ND = D / 16, NQ = D / 64;
   typedef typename std::conditional<F32, float, uint16_t>::type IO;
   __shared__ float so[4][16][D + 4];
@@ -282,9 +277,11 @@ __global__ __launch_bounds__(256, 2) void kv_attend_few_kernel(KvAttendArgs a) {
         k[t][s] = *reinterpret_cast<const u32x4*>(kb + ((4 * s + quad) * 64 + 16 * (col >> 2) + 4 * t + (col & 3)) * 16);
 #pragma unroll
     for (int d = 0; d < ND; ++d) v[d] = *reinterpret_cast<const u32x4*>(vb + (quad * D + 16 * d + col) * 16);
-    const float ck = cq * walk.k_scale(slot);
-    float factor;
-    const int delta = enter_block(ev_cur, walk.v_exponent(slot), factor);
+    float ks, factor;
+    int ev;
+    walk.scales(slot, ks, ev);
+    const float ck = cq * ks;
+    const int delta = enter_block(ev_cur, ev, factor);
 
     f32x4 s4[4];
 #pragma unroll
@@ -404,7 +401,6 @@ __global__ __launch_bounds__(256, 2) void kv_attend_few_kernel(KvAttendArgs a) {
     l = 0.0f;
 #pragma unroll
     for (int i = 0; i < ND / 4; ++i) x[i] = f32x4{0, 0, 0, 0};
-#pragma unroll 2
     for (int s = 0; s < parts; ++s) {
       const float2 ml = get_pair(&a.part_ml[s * all + at].x);
       float2 y[ND / 2];

@@ -15,17 +15,15 @@ struct rc_kv_plan {
   void* ws = nullptr;  // partial results: outputs, (m, l), numbers of parts
   size_t ws_bytes = 0;
   int64_t part_rows = 0;  // rows of partial results that it holds
-  uint32_t* arrived = nullptr;  // [kFewBlocks], after them
+  uint32_t* arrived = nullptr;  // [kFewGroups], after them
 };
 
 namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Blocks of threads that the kernel for few rows is split into, where there are
-// fewer groups of rows: two for each that the CUs hold at once (three), so that the
-// ragged ends of sequences even out.
-constexpr int64_t kFewBlocks = 1536;
+// Groups of rows of the kernel for few rows that may have several parts, at most.
+constexpr int64_t kFewGroups = 1536;
 
 // How a call runs: which kernel, and in how many parts of which length a group of
 // rows reads its blocks.
@@ -46,7 +44,20 @@ Way way_of(const rc_kv_plan* pl, int64_t queries, int64_t blocks, bool chosen, i
   blocks = std::max<int64_t>(blocks, 1);
   if (w.few) {
     const int64_t base = heads * (own_lists ? queries * ceil_div(group, 16) : ceil_div(rows, 16));
-    splits = std::min({ceil_div(kFewBlocks, base), ceil_div(blocks, 4), most_rows / (heads * rows)});
+    // The time in steps of one block a wave: rounds of the blocks of threads that the
+    // CUs hold at once, each with what its start and end cost (measured over 2 KB to
+    // 64 KB tokens: whole rounds win; 102 us in one round against 109 in 1.3 and 111 in
+    // two, for 32 sequences of 8192 tokens and 8 key heads of 128).
+    const int64_t at_once = 256 * (s.head_dim == 128 ? (pl->dtype == RC_F32 ? 2 : 3) : 4);
+    const int64_t most = base <= kFewGroups ? std::min({ceil_div(blocks, 4), most_rows / (heads * rows), (int64_t)1024}) : 1;
+    double best = 0.0;
+    for (int64_t p = 1; p <= std::max<int64_t>(most, 1); ++p) {
+      const double cost = (double)ceil_div(base * p, at_once) * ((double)ceil_div(ceil_div(blocks, p), 4) + 0.6);
+      if (p == 1 || cost < best) {
+        best = cost;
+        splits = p;
+      }
+    }
   } else {
     // Blocks of threads that a CU holds at once (registers and LDS of the kernel).
     const bool f32 = pl->dtype == RC_F32;
@@ -215,7 +226,7 @@ rc_status_t rc_kv_plan_create(rc_kv_shape_t shape, rc_dtype_t dtype, const rc_kv
   pl->params = *params;
   pl->part_rows = part_rows_at_most(pl);
   if (pl->part_rows) {
-    const size_t parts = part_bytes(pl, pl->part_rows), counts = kFewBlocks * sizeof(uint32_t);
+    const size_t parts = part_bytes(pl, pl->part_rows), counts = kFewGroups * sizeof(uint32_t);
     if (hipMalloc(&pl->ws, parts + counts) != hipSuccess) {
       delete pl;
       return RC_ERR_HIP;
