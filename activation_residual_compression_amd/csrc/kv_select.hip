@@ -21,15 +21,56 @@ __device__ __forceinline__ uint32_t sort_key(float x) {
   return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-template <int D, typename IN>
-__global__ __launch_bounds__(256) void kv_select_kernel(KvAttendArgs a) {
+// From a lane and the one that CTRL pairs it with (they differ in the bit that `high`
+// tells): the larger of the two values of the half of the registers that the lane keeps.
+template <int N, int CTRL>
+__device__ __forceinline__ void max_halve(float (&r)[16], bool high) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const float keep = high ? r[i + N / 2] : r[i], send = high ? r[i] : r[i + N / 2];
+    r[i] = fmaxf(keep, dpp_f32<CTRL>(send));
+  }
+}
+// Maxima over 32 lanes of 16 registers: lane l gets that of register
+// 8 * bit 4 + 4 * bit 3 + 2 * bit 2 + bit 1 of l.
+__device__ __forceinline__ float max_rows(float (&r)[16], int l) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(r[i]), __float_as_uint(r[i + 8]), false, false);
+    r[i] = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+  }
+  constexpr int kRowRor8 = 0x128;
+  max_halve<8, kRowRor8>(r, l & 8);
+  max_halve<4, kHalfMirror>(r, l & 4);
+  max_halve<2, kQuadXor2>(r, l & 2);
+  return fmaxf(r[0], dpp_f32<kQuadXor1>(r[0]));
+}
+
+// Inclusive sum over the lanes up to this one.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t add_from(uint32_t v) {
+  return v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ uint32_t sum_up_to(uint32_t v) {
+  v = add_from<0x111, 0xF>(v);  // from the lane 1, 2, 4, 8 below in the row of 16
+  v = add_from<0x112, 0xF>(v);
+  v = add_from<0x114, 0xF>(v);
+  v = add_from<0x118, 0xF>(v);
+  v = add_from<0x142, 0xA>(v);  // the last lane of row 0 to row 1, of row 2 to row 3
+  return add_from<0x143, 0xC>(v);  // lane 31 to rows 2 and 3
+}
+
+template <int D, typename IN, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void kv_select_kernel(KvAttendArgs a) {
   constexpr int QS = D + 16;  // LDS row of query codes
   extern __shared__ uint32_t keys[];
   __shared__ __align__(16) uint8_t qc[kRows * QS];
   __shared__ float qs[kRows];
   __shared__ int qlim[kRows];
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t pick[2];
+  constexpr int THREADS = 64 * WAVES;
+  __shared__ uint32_t hist[4][256];
+  __shared__ int2 count[WAVES];
+  __shared__ __align__(16) float ks[WAVES][64];
   const KvGeom& g = a.g;
   const int b = blockIdx.z, h = blockIdx.y, tile = blockIdx.x, G = g.group;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l32 = lane & 31, half = lane >> 5;
@@ -37,18 +78,20 @@ __global__ __launch_bounds__(256) void kv_select_kernel(KvAttendArgs a) {
   const int q0 = tile * a.q_tile, rows = min(a.q_tile, a.queries - q0) * G;
   const int lim_lo = kv_limit(a, len, q0), lim_hi = kv_limit(a, len, q0 + rows / G - 1);
   const int nb = (lim_hi + 63) / 64;
-  for (int j = tid; j < nb; j += 256) keys[j] = 0;
+  for (int j = tid; j < nb; j += THREADS) keys[j] = 0;
+  for (int i = tid; i < 4 * 256; i += THREADS) (&hist[0][0])[i] = 0;
 
   for (int r0 = 0; r0 < rows; r0 += kRows) {
     __syncthreads();
     {
-      const int r = tid >> 1, c0 = (tid & 1) * (D / 2);
+      constexpr int TPR = THREADS / kRows, N = D / TPR;  // threads of a row, values of each
+      const int r = tid / TPR, c0 = tid % TPR * N;
       const bool live = r0 + r < rows;
       const int i = q0 + (r0 + r) / G, hq = h * G + (r0 + r) % G;
-      float x[D / 2];
+      float x[N];
       float top = 0.0f;
 #pragma unroll
-      for (int c = 0; c < D / 2; c += 8) {
+      for (int c = 0; c < N; c += 8) {
         float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (live) row8<IN>((const IN*)a.q.data + b * a.q.sb + (int64_t)i * a.q.st + hq * a.q.sh + c0 + c, y);
 #pragma unroll
@@ -57,137 +100,155 @@ __global__ __launch_bounds__(256) void kv_select_kernel(KvAttendArgs a) {
           top = fmaxf(top, fabsf(y[u]));
         }
       }
-      top = fmaxf(top, dpp_f32<kQuadXor1>(top));
+      top = group_max<TPR>(top);
       const float up = top > 0.0f ? 127.0f * (1.0f / top) : 0.0f;
 #pragma unroll
-      for (int c = 0; c < D / 2; c += 4) {
+      for (int c = 0; c < N; c += 4) {
         uint32_t w = 0;
 #pragma unroll
         for (int u = 0; u < 4; ++u) w |= ((uint32_t)(int)rintf(x[c + u] * up) & 255u) << (8 * u);
         *reinterpret_cast<uint32_t*>(qc + r * QS + c0 + c) = w;
       }
-      if ((tid & 1) == 0) {
+      if (tid % TPR == 0) {
         qs[r] = top;
         qlim[r] = live ? kv_limit(a, len, i) : 0;
       }
     }
     __syncthreads();
     const int cols = min(rows - r0, kRows);
-    for (int bt = wave * 32; bt < nb; bt += 128) {
-      const int j = bt + l32;
-      const int block = j < nb ? kv_block(g, b, j) : -1;
-      const int64_t row = block < 0 ? 0 : kv_row(g, block, h);
-      i32x4 m[D / 32];
+    for (int b64 = wave * 64; b64 < nb; b64 += THREADS) {
+      // two tiles of 32 blocks, all their loads first. A block that does not exist has a
+      // mean of scale NaN, which no maximum takes.
+      const int mine = b64 + lane < nb ? kv_block(g, b, b64 + lane) : -1;
+      i32x4 mean[2][D / 32];
+      ks[wave][lane] = mine < 0 ? __builtin_nanf("") : g.k_mean_scale[kv_row(g, mine, h)];
 #pragma unroll
-      for (int s = 0; s < D / 32; ++s)
-        m[s] = block < 0 ? i32x4{0, 0, 0, 0}
-                         : *reinterpret_cast<const i32x4*>(g.k_mean + row * D + s * 32 + half * 16);
-      const float ks = block < 0 ? 0.0f : g.k_mean_scale[row];
-      float best[16], ksr[16];
+      for (int u = 0; u < 2; ++u) {
+        const int block = __shfl(mine, 32 * u + l32);
+        const int64_t row = kv_row(g, max(block, 0), h);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        best[i] = -INFINITY;
-        ksr[i] = __shfl(ks, 8 * (i / 4) + 4 * half + i % 4);
-      }
-      for (int ct = 0; ct < cols; ct += 32) {
-        i32x16 acc = {};
-#pragma unroll
-        for (int s = 0; s < D / 32; ++s) {
-          const i32x4 q = *reinterpret_cast<const i32x4*>(qc + (ct + l32) * QS + s * 32 + half * 16);
-          acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(m[s], q, acc, 0, 0, 0);
-        }
-        const float mul = qs[ct + l32];
-        const int seen = (qlim[ct + l32] + 63) / 64 - bt;  // rows below: blocks whose first token is seen
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float v = (float)acc[i] * ksr[i] * mul + 0.0f;  // + 0: -0 and 0 tie
-          if (8 * (i / 4) + 4 * half + i % 4 < seen) best[i] = fmaxf(best[i], v);
-        }
+        for (int s = 0; s < D / 32; ++s)
+          mean[u][s] = *reinterpret_cast<const i32x4*>(g.k_mean + row * D + s * 32 + half * 16);
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float v = group_max<32>(best[i]);
-        const int jj = bt + 8 * (i / 4) + 4 * half + i % 4;
-        if (l32 == i && jj < nb) keys[jj] = max(keys[jj], sort_key(v));
+      for (int u = 0; u < 2; ++u) {
+        const int bt = b64 + 32 * u;
+        if (bt >= nb) break;
+        float best[16];  // register i: block bt + 8 (i / 4) + 4 half + i % 4
+        f32x4 scale[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) scale[i] = *reinterpret_cast<const f32x4*>(&ks[wave][32 * u + 8 * i + 4 * half]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) best[i] = -INFINITY;
+        for (int ct = 0; ct < cols; ct += 32) {
+          i32x16 acc = {};
+#pragma unroll
+          for (int s = 0; s < D / 32; ++s) {
+            const i32x4 q = *reinterpret_cast<const i32x4*>(qc + (ct + l32) * QS + s * 32 + half * 16);
+            acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(mean[u][s], q, acc, 0, 0, 0);
+          }
+          const float mul = qs[ct + l32];
+          const int seen = (qlim[ct + l32] + 63) / 64 - bt;  // blocks of the tile whose first token is seen
+          const bool some = __any(seen < 32);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float v = (float)acc[i] * scale[i / 4][i % 4] * mul + 0.0f;  // + 0: -0 and 0 tie
+            if (some && 8 * (i / 4) + 4 * half + i % 4 >= seen) v = -INFINITY;
+            best[i] = fmaxf(best[i], v);
+          }
+        }
+        const float v = max_rows(best, l32);
+        const int jj = bt + 8 * (l32 >> 3) + 4 * half + (l32 >> 1 & 3);
+        if ((l32 & 1) == 0 && jj < nb) keys[jj] = max(keys[jj], sort_key(v));
       }
     }
   }
   __syncthreads();
   const int own0 = (max(lim_lo, 1) - 1) / 64;
-  for (int j = tid; j < nb; j += 256) {
-    uint32_t k = keys[j];
-    if (a.causal && j >= own0) k = 0xFFFFFFFFu;
-    if (kv_block(g, b, j) < 0) k = 0;
-    keys[j] = k;
+  for (int j = tid; j < nb; j += THREADS) {
+    if (a.causal && j >= own0 && keys[j] > kNone) keys[j] = 0xFFFFFFFFu;
   }
-  // radix select: the key of the keep-th best, and how many of that key are taken
+  __syncthreads();
+  // radix select: the key of the keep-th best, and how many of that key are taken. Every
+  // wave works out each digit for itself, so a digit costs one barrier.
   uint32_t prefix = 0, want = (uint32_t)a.keep;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    hist[tid] = 0;
-    __syncthreads();
-    for (int j = tid; j < nb; j += 256) {
+  bool all = false;
+  for (int digit = 0; digit < 4; ++digit) {
+    const int shift = 24 - 8 * digit;
+    for (int j = tid; j < nb; j += THREADS) {
       const uint32_t k = keys[j];
-      if (k > kNone && (shift == 24 || k >> (shift + 8) == prefix)) atomicAdd(&hist[k >> shift & 255u], 1u);
+      if (k > kNone && (digit == 0 || k >> (shift + 8) == prefix)) atomicAdd(&hist[digit][k >> shift & 255u], 1u);
     }
     __syncthreads();
-    if (wave == 0) {
-      uint32_t c[4], sum = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum += c[i] = hist[4 * lane + i];
-      uint32_t above = sum;  // entries in this lane's bins and the higher ones
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_down((int)above, d);
-        if (lane + d < 64) above += o;
-      }
-      uint32_t higher = above - sum;
-      if (lane == 0 && above < want) {  // fewer than wanted: take all
-        pick[0] = 0;
-        pick[1] = 0xFFFFFFFFu;
-      }
-      if (above >= want && higher < want) {
-#pragma unroll
-        for (int i = 3; i >= 0; --i) {
-          if (higher < want && higher + c[i] >= want) {
-            pick[0] = 4 * lane + i;
-            pick[1] = want - higher;
-          }
-          higher += c[i];
-        }
-      }
+    // lane l: bins 255 - 4 l and the three below it
+    const uint4 bins = *reinterpret_cast<const uint4*>(&hist[digit][252 - 4 * lane]);
+    const uint32_t c[4] = {bins.w, bins.z, bins.y, bins.x}, sum = bins.x + bins.y + bins.z + bins.w;
+    const uint32_t up_to = sum_up_to(sum);  // entries in this lane's bins and the higher ones
+    if ((uint32_t)__builtin_amdgcn_readlane((int)up_to, 63) < want) {  // only at the first digit
+      all = true;
+      break;
     }
-    __syncthreads();
-    if (pick[1] == 0xFFFFFFFFu) break;  // only at the first digit: later ones hold at least `want`
-    prefix = prefix << 8 | pick[0];
-    want = pick[1];
-    __syncthreads();
+    const int at = __builtin_ctzll(__ballot(up_to >= want));
+    uint32_t higher = up_to - sum, bin = 0, rest = 0;
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!found && higher + c[i] >= want) {
+        found = true;
+        bin = 255u - 4u * (uint32_t)lane - (uint32_t)i;
+        rest = want - higher;
+      }
+      higher += c[i];
+    }
+    prefix = prefix << 8 | (uint32_t)__builtin_amdgcn_readlane((int)bin, at);
+    want = (uint32_t)__builtin_amdgcn_readlane((int)rest, at);
   }
-  const bool all = pick[1] == 0xFFFFFFFFu;
-  if (wave == 0) {
-    int32_t* out = a.blocks_out + (((int64_t)b * g.kv_heads + h) * a.tiles + tile) * a.keep;
-    int n = 0;
-    uint32_t ties = 0;
-    const uint64_t below = ((uint64_t)1 << lane) - 1;
-    for (int j0 = 0; j0 < nb; j0 += 64) {
-      const int j = j0 + lane;
-      const uint32_t k = j < nb ? keys[j] : 0;
-      const bool ok = k > kNone;
-      const bool tie = ok && !all && k == prefix;
-      const uint64_t tied = __ballot(tie);
-      const bool take = ok && (all || k > prefix || (tie && ties + __popcll(tied & below) < want));
-      const uint64_t taken = __ballot(take);
-      if (take) out[n + __popcll(taken & below)] = j;
-      n += __popcll(taken);
-      ties += __popcll(tied);
-    }
-    for (int i = n + lane; i < a.keep; i += 64) out[i] = -1;
+  // the taken ones in order: each wave has a run of blocks, and first counts
+  const int run = ((nb + WAVES - 1) / WAVES + 63) & ~63, j_end = min((wave + 1) * run, nb);
+  int over = 0, ties = 0;
+  for (int j0 = wave * run; j0 < j_end; j0 += 64) {
+    const uint32_t k = j0 + lane < j_end ? keys[j0 + lane] : 0;
+    over += __popcll(__ballot(k > kNone && (all || k > prefix)));
+    ties += __popcll(__ballot(k > kNone && !all && k == prefix));
   }
+  if (lane == 0) count[wave] = make_int2(over, ties);
+  __syncthreads();
+  int n = 0, tied = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    const int2 c = count[w];
+    if (w < wave) {
+      n += c.x;
+      tied += c.y;
+    }
+    over = w == 0 ? c.x : over + c.x;
+    ties = w == 0 ? c.y : ties + c.y;
+  }
+  n += min(tied, (int)want);
+  int32_t* out = a.blocks_out + (((int64_t)b * g.kv_heads + h) * a.tiles + tile) * a.keep;
+  const uint64_t below = ((uint64_t)1 << lane) - 1;
+  for (int j0 = wave * run; j0 < j_end; j0 += 64) {
+    const uint32_t k = j0 + lane < j_end ? keys[j0 + lane] : 0;
+    const bool tie = k > kNone && !all && k == prefix;
+    const uint64_t same = __ballot(tie);
+    const bool take = k > kNone && (all || k > prefix || (tie && tied + __popcll(same & below) < (int)want));
+    const uint64_t taken = __ballot(take);
+    if (take) out[n + __popcll(taken & below)] = j0 + lane;
+    n += __popcll(taken);
+    tied += __popcll(same);
+  }
+  for (int i = over + min(ties, (int)want) + tid; i < a.keep; i += THREADS) out[i] = -1;
 }
 
+// 8 waves score the blocks of a tile where the tiles are too few to fill the CUs.
 template <int D, typename IN>
 hipError_t run(const KvAttendArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.tiles, (unsigned)a.g.kv_heads, (unsigned)a.g.batch);
-  kv_select_kernel<D, IN><<<grid, 256, (size_t)((a.max_len + 63) / 64) * 4, s>>>(a);
+  const int blocks = (a.max_len + 63) / 64;
+  if ((int64_t)a.tiles * a.g.kv_heads * a.g.batch <= 512 && blocks > 256)
+    kv_select_kernel<D, IN, 8><<<grid, 512, (size_t)blocks * 4, s>>>(a);
+  else
+    kv_select_kernel<D, IN, 4><<<grid, 256, (size_t)blocks * 4, s>>>(a);
   return hipGetLastError();
 }
 
