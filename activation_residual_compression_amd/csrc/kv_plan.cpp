@@ -44,15 +44,19 @@ Way way_of(const rc_kv_plan* pl, int64_t queries, int64_t blocks, bool chosen, i
   blocks = std::max<int64_t>(blocks, 1);
   if (w.few) {
     const int64_t base = heads * (own_lists ? queries * ceil_div(group, 16) : ceil_div(rows, 16));
-    // The time in steps of one block a wave: rounds of the blocks of threads that the
-    // CUs hold at once, each with what its start and end cost (measured over 2 KB to
-    // 64 KB tokens: whole rounds win; 102 us in one round against 109 in 1.3 and 111 in
-    // two, for 32 sequences of 8192 tokens and 8 key heads of 128).
+    // The time in microseconds: the bytes at 5.8 TB/s, or the waves' blocks one after
+    // the other (2.4 each) where that is longer; 4 for the start and end of a round of
+    // the blocks of threads that the CUs hold at once; for the join 5, and 0.4 for each
+    // part. Measured: 32 sequences of 8192 tokens, 8 key heads of 128, 95 us in one part
+    // and 103, 102, 108, 111 in 2, 3, 4, 6; 4 of 65536 tokens 108 us in 7 parts, 110 in
+    // 24, 118 in 32; 8 of 32 chosen blocks 12.0 us in 4, 13.7 in 8, 13.1 in 2.
     const int64_t at_once = 256 * (s.head_dim == 128 ? (pl->dtype == RC_F32 ? 2 : 3) : 4);
-    const int64_t most = base <= kFewGroups ? std::min({ceil_div(blocks, 4), most_rows / (heads * rows), (int64_t)1024}) : 1;
+    const int64_t most = base <= kFewGroups ? std::min({ceil_div(blocks, 4), most_rows / (heads * rows), (int64_t)256}) : 1;
+    const double read_us = (double)base * (double)blocks * (128.0 * s.head_dim) / 5.8e6;
     double best = 0.0;
     for (int64_t p = 1; p <= std::max<int64_t>(most, 1); ++p) {
-      const double cost = (double)ceil_div(base * p, at_once) * ((double)ceil_div(ceil_div(blocks, p), 4) + 0.6);
+      const double rounds = (double)ceil_div(base * p, at_once), steps = (double)ceil_div(ceil_div(blocks, p), 4);
+      const double cost = std::max(read_us, rounds * steps * 2.4) + 4.0 * rounds + (p > 1 ? 5.0 + 0.4 * (double)p : 0.0);
       if (p == 1 || cost < best) {
         best = cost;
         splits = p;
