@@ -38,6 +38,7 @@ struct KvStoreArgs {
   const int32_t* start;
   const int32_t* count;  // or null
   int tokens;
+  bool once;  // the inputs are larger than half the last-level cache (256 MB)
 };
 hipError_t launch_kv_store(const KvStoreArgs& a, bool k_bf16, bool v_bf16, hipStream_t s);
 

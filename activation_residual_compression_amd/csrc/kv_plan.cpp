@@ -264,6 +264,8 @@ rc_status_t rc_kv_store(rc_kv_plan_t pl, hipStream_t stream, const rc_kv_cache_t
   a.start = start;
   a.count = count;
   a.tokens = tokens;
+  a.once = (int64_t)s.batch * tokens * s.kv_heads * s.head_dim *
+               ((k->dtype == RC_BF16 ? 2 : 4) + (v->dtype == RC_BF16 ? 2 : 4)) > (int64_t)128 << 20;
   return rc::launch_kv_store(a, k->dtype == RC_BF16, v->dtype == RC_BF16, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
 }
 

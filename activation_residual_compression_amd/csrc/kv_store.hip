@@ -32,13 +32,43 @@ __device__ __forceinline__ int exponent_for(uint32_t amax_bits) {
   return min(max(e, kKvEMin), kKvEMax);
 }
 
-template <int D, typename KIN, typename VIN>
+// 4 x 4 bytes, rows to columns: byte i of c[j] is byte j of r[i].
+__device__ __forceinline__ void turn4(const uint32_t (&r)[4], uint32_t (&c)[4]) {
+  const uint32_t ab_lo = __builtin_amdgcn_perm(r[1], r[0], 0x05010400u), ab_hi = __builtin_amdgcn_perm(r[1], r[0], 0x07030602u);
+  const uint32_t cd_lo = __builtin_amdgcn_perm(r[3], r[2], 0x05010400u), cd_hi = __builtin_amdgcn_perm(r[3], r[2], 0x07030602u);
+  c[0] = __builtin_amdgcn_perm(cd_lo, ab_lo, 0x05040100u);
+  c[1] = __builtin_amdgcn_perm(cd_lo, ab_lo, 0x07060302u);
+  c[2] = __builtin_amdgcn_perm(cd_hi, ab_hi, 0x05040100u);
+  c[3] = __builtin_amdgcn_perm(cd_hi, ab_hi, 0x07060302u);
+}
+
+// 8 values of a row; once: past the caches. Inputs that fit the last-level cache are
+// often still there from what wrote them (a peer's reconstruction of 4444 x 1920 fp32,
+// read twice over: 15.7 us against 21.2 past the caches); larger ones only push other
+// data out (226 MB of bf16: 68 us past them, 75 through).
+template <typename IN, bool ONCE>
+__device__ __forceinline__ void row8_in(const IN* p, float (&x)[8]) {
+  if constexpr (ONCE) {
+    const f32x4 a = load4<IN>(p), b = load4<IN>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = a[i];
+      x[4 + i] = b[i];
+    }
+  } else {
+    row8<IN>(p, x);
+  }
+}
+
+template <int D, typename KIN, typename VIN, bool ONCE>
 __global__ __launch_bounds__(256) void kv_store_kernel(KvStoreArgs a) {
-  constexpr int W = D / 4;       // values of a thread: a quarter of a token's row
+  constexpr int ROW = D / 8, TURNS = 64 * ROW / 256;  // threads of a token's row, rows of a thread
   constexpr int LS = D + 16;     // LDS row of codes; 16 B of padding spread the columns over the banks
+  constexpr int UNITS = 64 * D / 16 / 256;  // 16-byte units of a thread
+  constexpr int QUADS = D / 4, PARTS = 256 / QUADS;
   __shared__ uint32_t wave_max[4];
   __shared__ __align__(16) uint8_t codes[64 * LS];
-  __shared__ float sums[2][D];
+  __shared__ __align__(16) float sums[PARTS][D];
   const KvGeom& g = a.g;
   const int b = blockIdx.z, head = blockIdx.y >> 1;
   const bool is_v = blockIdx.y & 1;
@@ -53,92 +83,99 @@ __global__ __launch_bounds__(256) void kv_store_kernel(KvStoreArgs a) {
   const int first = start > t0 ? (int)(start - t0) : 0;              // slots before: earlier tokens
   const int last = start + n < t0 + 64 ? (int)(start + n - t0) : 64;  // slots from here on: none
   const bool begun = first > 0;
+  const int64_t row = kv_row(g, block, head);
+  uint8_t* base = (is_v ? g.v : g.k) + row * (64 * D);
+  const int tid = threadIdx.x;
 
-  const int tid = threadIdx.x, t = tid >> 2, c0 = (tid & 3) * W;
-  const bool is_new = t >= first && t < last;
-  float x[W];
-#pragma unroll
-  for (int i = 0; i < W; ++i) x[i] = 0.0f;
-  if (is_new) {
-    const int64_t tok = t0 + t - start;
-#pragma unroll
-    for (int i = 0; i < W; i += 8) {
-      float y[8];
-      if (is_v)
-        row8<VIN>((const VIN*)a.v.data + b * a.v.sb + tok * a.v.st + head * a.v.sh + c0 + i, y);
-      else
-        row8<KIN>((const KIN*)a.k.data + b * a.k.sb + tok * a.k.st + head * a.k.sh + c0 + i, y);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) x[i + u] = y[u];
-    }
-  }
+  float x[TURNS][8];
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const uint32_t u = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-    top = max(top, u < 0x7F800000u ? u : 0u);
+  for (int i = 0; i < TURNS; ++i) {
+    const int t = tid / ROW + 256 / ROW * i, c0 = tid % ROW * 8;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) x[i][u] = 0.0f;
+    if (t >= first && t < last) {
+      const int64_t tok = t0 + t - start;
+      if (is_v)
+        row8_in<VIN, ONCE>((const VIN*)a.v.data + b * a.v.sb + tok * a.v.st + head * a.v.sh + c0, x[i]);
+      else
+        row8_in<KIN, ONCE>((const KIN*)a.k.data + b * a.k.sb + tok * a.k.st + head * a.k.sh + c0, x[i]);
+    }
   }
+  // K's earlier codes, as units of the layout [D/16][64][16]
+  u32x4 was[UNITS];
+  if (begun && !is_v) {
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u)
+      if ((tid & 63) < first) was[u] = *reinterpret_cast<const u32x4*>(base + (tid + 256 * u) * 16);
+  }
+#pragma unroll
+  for (int i = 0; i < TURNS; ++i)
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t v = __float_as_uint(x[i][u]) & 0x7FFFFFFFu;
+      top = max(top, v < 0x7F800000u ? v : 0u);
+    }
   top = group_max_u32<32>(top);
   top = max(top, (uint32_t)__shfl_xor((int)top, 32));
   if ((tid & 63) == 0) wave_max[tid >> 6] = top;
-  __syncthreads();
-  top = max(max(wave_max[0], wave_max[1]), max(wave_max[2], wave_max[3]));
-
-  const int64_t row = kv_row(g, block, head);
   float* scale = (is_v ? g.v_scale : g.k_scale) + row;
   const int e_was = begun ? scale_exponent(*scale) : kKvEMin;
+  __syncthreads();
+  top = max(max(wave_max[0], wave_max[1]), max(wave_max[2], wave_max[3]));
   const int e = begun ? max(exponent_for(top), e_was) : exponent_for(top);
   const bool again = begun && e > e_was;
   const float inv = pow2f(-e), down = pow2f(e_was - e);
-  uint8_t* base = (is_v ? g.v : g.k) + row * (64 * D);
 
-  uint32_t w[W / 4];
 #pragma unroll
-  for (int i = 0; i < W / 4; ++i) w[i] = encode4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], inv);
-
-  if (!is_v) {
-    // K: a thread's values are 16-byte units of the layout [D/16][64][16]
+  for (int i = 0; i < TURNS; ++i) {
+    const int t = tid / ROW + 256 / ROW * i, c0 = tid % ROW * 8;
+    if (t >= first)
+      *reinterpret_cast<u32x2*>(codes + t * LS + c0) = u32x2{encode4(x[i][0], x[i][1], x[i][2], x[i][3], inv),
+                                                             encode4(x[i][4], x[i][5], x[i][6], x[i][7], inv)};
+  }
+  if (begun && !is_v && (tid & 63) < first) {
 #pragma unroll
-    for (int u = 0; u < W / 16; ++u) {
-      u32x4* unit = reinterpret_cast<u32x4*>(base + ((c0 / 16 + u) * 64 + t) * 16);
-      if (t < first) {
-        const u32x4 was = *unit;
-        w[4 * u] = was.x; w[4 * u + 1] = was.y; w[4 * u + 2] = was.z; w[4 * u + 3] = was.w;
-        if (again) {
+    for (int u = 0; u < UNITS; ++u) {
+      if (again) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[4 * u + i] = recode4(w[4 * u + i], down);
-        }
+        for (int i = 0; i < 4; ++i) was[u][i] = recode4(was[u][i], down);
       }
-      if (!begun || is_new || (again && t < first))
-        *unit = u32x4{w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]};
+      *reinterpret_cast<u32x4*>(codes + (tid & 63) * LS + ((tid + 256 * u) >> 6) * 16) = was[u];
     }
   }
-#pragma unroll
-  for (int i = 0; i < W / 4; ++i) *reinterpret_cast<uint32_t*>(codes + t * LS + c0 + 4 * i) = w[i];
   __syncthreads();
 
   if (!is_v) {
-    // mean key: sums of at most 64 codes are whole multiples of 2^-9 below 2^15, exact in fp32
-    constexpr int PARTS = 256 / D, SPAN = 64 / PARTS;
-    const int d = tid % D, part = tid / D;
-    float s = 0.0f;
-    for (int i = part * SPAN; i < min(last, (part + 1) * SPAN); ++i) {
-      const float c = value_of(codes[i * LS + d]);
-      s += c == c ? c : 0.0f;  // NaN counts as 0
+    const int t = tid & 63;
+    if (!begun || (t >= first && t < last) || (again && t < first)) {
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u)
+        *reinterpret_cast<u32x4*>(base + (tid + 256 * u) * 16) =
+            *reinterpret_cast<const u32x4*>(codes + t * LS + ((tid + 256 * u) >> 6) * 16);
     }
-    if constexpr (PARTS == 4) {
-      // D = 64: a wave holds one part; fold the four by way of LDS in two steps
-      if (part >= 2) sums[part - 2][d] = s;
-      __syncthreads();
-      if (part < 2) s += sums[part][d];
-      __syncthreads();
+    // mean key: sums of at most 64 codes are whole multiples of 2^-9 below 2^15, exact in
+    // fp32 in any order
+    const int quad = tid % QUADS, part = tid / QUADS;
+    f32x4 s = {0, 0, 0, 0};
+#pragma unroll 2
+    for (int i = part * (64 / PARTS); i < (part + 1) * (64 / PARTS); ++i) {
+      uint32_t w = *reinterpret_cast<const uint32_t*>(codes + i * LS + 4 * quad);
+      if (i >= last) w = 0;
+      const f32x4 c = {__builtin_amdgcn_cvt_f32_fp8(w, 0), __builtin_amdgcn_cvt_f32_fp8(w, 1),
+                       __builtin_amdgcn_cvt_f32_fp8(w, 2), __builtin_amdgcn_cvt_f32_fp8(w, 3)};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] += c[k] == c[k] ? c[k] : 0.0f;  // NaN counts as 0
     }
-    if (part == 1) sums[1][d] = s;
-    __syncthreads();
-    if (part == 0) sums[0][d] = s + sums[1][d];
+    *reinterpret_cast<f32x4*>(&sums[part][4 * quad]) = s;
     __syncthreads();
     if (tid < 64) {
-      const float s0 = sums[0][tid], s1 = D == 128 ? sums[0][tid + D / 2] : 0.0f;
+      float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) {
+        s0 += sums[p][tid];
+        if (D == 128) s1 += sums[p][tid + D / 2];
+      }
       uint32_t m = max(__float_as_uint(s0) & 0x7FFFFFFFu, __float_as_uint(s1) & 0x7FFFFFFFu);
       m = group_max_u32<32>(m);
       m = max(m, (uint32_t)__shfl_xor((int)m, 32));
@@ -153,16 +190,34 @@ __global__ __launch_bounds__(256) void kv_store_kernel(KvStoreArgs a) {
       }
     }
   } else {
-    // V: a unit is 16 tokens of one channel, layout [4][D][16]: the codes turn in LDS
+    // V: a unit is 16 tokens of one channel, layout [4][D][16]: the codes turn, 4 channels
+    // and 16 tokens a thread
     if (tid == 0) *scale = pow2f(e);
+    if (!begun) {
+      if (tid >= D) return;
+      const int lo = tid / QUADS * 16, c0 = tid % QUADS * 4;
+      uint32_t out[4][4];  // [channel][4 tokens]
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t r[4], c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = *reinterpret_cast<const uint32_t*>(codes + (lo + 4 * q + i) * LS + c0);
+        turn4(r, c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[k][q] = c[k];
+      }
+      u32x4* at = reinterpret_cast<u32x4*>(base + (lo / 16 * D + c0) * 16);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) at[k] = u32x4{out[k][0], out[k][1], out[k][2], out[k][3]};
+      return;
+    }
+    // beside earlier tokens: only the units that change, one a thread
     for (int unit = tid; unit < 4 * D; unit += 256) {
-      const int gq = unit / D, d = unit % D, lo = 16 * gq;
+      const int lo = unit / D * 16, d = unit % D;
       const bool any_new = lo < last && lo + 16 > first;
-      if (begun && !any_new && !(again && lo < first)) continue;
-      u32x4* at = reinterpret_cast<u32x4*>(base + (gq * D + d) * 16);
-      const bool need = begun && (lo < first || lo + 16 > last);
-      const u32x4 was = need ? *at : u32x4{0, 0, 0, 0};
-      uint32_t out[4] = {was.x, was.y, was.z, was.w};
+      if (!any_new && !(again && lo < first)) continue;
+      u32x4* at = reinterpret_cast<u32x4*>(base + unit * 16);
+      u32x4 out = *at;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint32_t re = again ? recode4(out[q], down) : out[q];
@@ -176,7 +231,7 @@ __global__ __launch_bounds__(256) void kv_store_kernel(KvStoreArgs a) {
         }
         out[q] = r;
       }
-      *at = u32x4{out[0], out[1], out[2], out[3]};
+      *at = out;
     }
   }
 }
@@ -184,7 +239,10 @@ __global__ __launch_bounds__(256) void kv_store_kernel(KvStoreArgs a) {
 template <int D, typename KIN, typename VIN>
 hipError_t run(const KvStoreArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)((a.tokens + 63) / 64 + 1), (unsigned)(2 * a.g.kv_heads), (unsigned)a.g.batch);
-  kv_store_kernel<D, KIN, VIN><<<grid, 256, 0, s>>>(a);
+  if (a.once)
+    kv_store_kernel<D, KIN, VIN, true><<<grid, 256, 0, s>>>(a);
+  else
+    kv_store_kernel<D, KIN, VIN, false><<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 template <int D>
