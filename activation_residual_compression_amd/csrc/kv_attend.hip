@@ -485,8 +485,10 @@ __device__ __forceinline__ float max_halves(float x) {
 // the softmax of half x and the first product of half x + 1 do not depend on each
 // other and are interleaved. K is therefore one block ahead of V in LDS (two buffers
 // of each, one barrier a block), and the global loads are one block ahead of that.
+// Waves of a SIMD: what the registers allow (D = 64 in 2 instead of 3: 830 us for the
+// video share instead of 780; fp32 at D = 128 in 2 would spill).
 template <int D, bool F32>
-__global__ __launch_bounds__(256, D == 128 && F32 ? 1 : 2) void kv_attend_many_kernel(KvAttendArgs a) {
+__global__ __launch_bounds__(256, D == 128 ? (F32 ? 1 : 2) : (F32 ? 2 : 3)) void kv_attend_many_kernel(KvAttendArgs a) {
   constexpr int NK = D / 16, ND = D / 32, UNITS = 64 * D / 16 / 256;
   typedef typename std::conditional<F32, float, uint16_t>::type IO;
   __shared__ half8_t sk[2][D / 8][64];  // [channel / 8][operand row]
@@ -652,10 +654,8 @@ __global__ __launch_bounds__(256, D == 128 && F32 ? 1 : 2) void kv_attend_many_k
       if (i == SLOTS - 2) between();
       if (i >= SLOTS - 2) {
 #pragma unroll
-        for (int k = 0; k < AHEAD / 2; ++k) {
-          const int n = (i - SLOTS + 2) * (AHEAD / 2) + k;
+        for (int n = (i - SLOTS + 2) * AHEAD / 2; n < (i - SLOTS + 3) * AHEAD / 2; ++n)
           first[n] = sk[nbuf][2 * n + half][32 * nu + col];
-        }
       }
       // the first product first: its results are then there when the next step begins
       if (i >= NK) {
@@ -722,8 +722,10 @@ __global__ __launch_bounds__(256, D == 128 && F32 ? 1 : 2) void kv_attend_many_k
       const int j2 = j1 >= 0 ? walk.next(block2, ks2, ev2) : -1;
       mask(sa, j, 0);
       step(sa, pa, la, pb, lb, buf ^ 1, 1, sb, buf, 1, ck, delta, sum, buf ^ 1, 0, [&](int i) {
-        // half a unit in each of 4 * UNITS slots: V, then K
-        constexpr int FROM = 1;
+        // half a unit in each of 4 * UNITS slots: V, then K; as late as the barrier allows
+        // where a block takes little time (D = 64: 824 us for the video share from slot 1,
+        // 770 from slot 2), since their loads were issued one block ago
+        constexpr int FROM = D == 64 ? 2 : 1;
         static_assert(FROM + 4 * UNITS <= SLOTS - 2 || UNITS == 0, "staged before the barrier");
         const int k = i - FROM, u = k / 2 % UNITS;
         if (k < 0 || k >= 4 * UNITS) return;
