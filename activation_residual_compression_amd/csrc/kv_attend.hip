@@ -35,6 +35,9 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 constexpr float kBias = 7.0f, kMost = 0x1p15f;  // f16 holds 2^15
 constexpr int kEvUp = 2, kEvDown = 8;
 constexpr float kLowest = -3.402823466e38f;
+// Rows of a block of threads of the kernel for many rows.
+template <int D, bool F32>
+constexpr int many_rows() { return D == 128 && F32 ? 32 : 64; }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -148,7 +151,8 @@ struct Walk {
   const int32_t* list;
   int b, h, base, to, step, lane;
   uint64_t left;  // entries of these 64 still to come
-  int lane_j, lane_block, lane_e;  // lane_e: the exponents of K's and V's scales, 16 bits each
+  int lane_block;
+  uint32_t lane_what;  // index (16 bits), exponents + 64 of K's and V's scales (8 bits each)
 
   __device__ __forceinline__ Walk(const KvGeom& g, const int32_t* list, int b, int h, int from, int to, int step,
                                   int lane)
@@ -158,12 +162,13 @@ struct Walk {
     lane_block = -1;
     const int at = base + lane * step;
     if (at < to) {
-      lane_j = list ? list[at] : at;
-      lane_block = kv_block(g, b, lane_j);
+      const int j = list ? list[at] : at;
+      lane_what = (uint32_t)j;
+      lane_block = kv_block(g, b, j);
     }
     if (lane_block >= 0) {
       const int64_t row = kv_row(g, lane_block, h);
-      lane_e = scale_exponent(g.k_scale[row]) << 16 | (scale_exponent(g.v_scale[row]) & 0xFFFF);
+      lane_what |= (uint32_t)(scale_exponent(g.k_scale[row]) + 64) << 16 | (uint32_t)(scale_exponent(g.v_scale[row]) + 64) << 24;
     }
     left = __ballot(lane_block >= 0);
   }
@@ -176,13 +181,13 @@ struct Walk {
     at = __builtin_ctzll(left);
     left &= left - 1;
     block = __builtin_amdgcn_readlane(lane_block, at);
-    return __builtin_amdgcn_readlane(lane_j, at);
+    return __builtin_amdgcn_readlane((int)lane_what, at) & 0xFFFF;
   }
   // Exponents of the scales of the block that next() found, before the next call of it.
   __device__ __forceinline__ void scales(int at, float& ks, int& ev) const {
-    const int e = __builtin_amdgcn_readlane(lane_e, at);
-    ks = pow2f(e >> 16);
-    ev = (int16_t)e;
+    const uint32_t what = (uint32_t)__builtin_amdgcn_readlane((int)lane_what, at);
+    ks = pow2f((int)(what >> 16 & 255u) - 64);
+    ev = (int)(what >> 24) - 64;
   }
   __device__ __forceinline__ int next(int& block, float& ks, int& ev) {
     int at;
@@ -476,37 +481,32 @@ __device__ __forceinline__ float max_halves(float x) {
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-// One block of threads: 128 rows of one key head (32 a wave). K and V of a block
-// are widened to f16 once, on their way into LDS, in the order of the operands, so
-// that every LDS read is one run of 64 lanes x 16 B.
-//
-// The matrix units and the exponentials take about as long as each other, so a wave
-// works on three half blocks (32 tokens) at once: the second product of half x - 1,
-// the softmax of half x and the first product of half x + 1 do not depend on each
-// other and are interleaved. K is therefore one block ahead of V in LDS (two buffers
-// of each, one barrier a block), and the global loads are one block ahead of that.
-// Waves of a SIMD: what the registers allow (D = 64 in 2 instead of 3: 830 us for the
-// video share instead of 780; fp32 at D = 128 in 2 would spill).
+// One block of threads: 64 rows of one key head, a part of the keys; its four waves
+// read blocks of their own straight into registers, as in the kernel for few rows, so
+// the loop has no barrier and no LDS write, and the waves of a SIMD drift apart: one
+// does its softmax while another feeds the matrix units. All rows' queries are in LDS,
+// written once; an operand of K or V serves two groups of 32 rows
+// (one for fp32 at 128 channels, whose registers hold no more). The waves are joined
+// in LDS at the end.
 template <int D, bool F32>
-__global__ __launch_bounds__(256, D == 128 ? (F32 ? 1 : 2) : (F32 ? 2 : 3)) void kv_attend_many_kernel(KvAttendArgs a) {
-  constexpr int NK = D / 16, ND = D / 32, UNITS = 64 * D / 16 / 256;
+__global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) {
+  constexpr int NK = D / 16, ND = D / 32, ROWS = many_rows<D, F32>(), U = ROWS / 32;
   typedef typename std::conditional<F32, float, uint16_t>::type IO;
-  __shared__ half8_t sk[2][D / 8][64];  // [channel / 8][operand row]
-  __shared__ half8_t sv[2][8][D];       // [token / 8][channel]
+  constexpr int QBYTES = (F32 ? 2 : 1) * NK * 2 * ROWS * 16, OBYTES = 2 * ROWS * (D + 4) * 4;
+  __shared__ __align__(16) char shared[QBYTES > OBYTES ? QBYTES : OBYTES];
+  __shared__ float2 sml[4][ROWS];
+  typedef half8_t QFrag[2][ROWS];
+  QFrag* sq = reinterpret_cast<QFrag*>(shared);  // [hi: NK, lo: NK][half][row]: 8 channels of a row
   const KvGeom& g = a.g;
   const int rows = a.queries * g.group;
-  const int row_tiles = (rows + 127) / 128;
+  const int row_tiles = (rows + ROWS - 1) / ROWS;
   const Place place = place_of(a, blockIdx.x, gridDim.x, row_tiles);
   const int b = place.b, h = place.h, split = place.split, tile = place.tile;
-  const int r0 = tile * 128;
+  const int r0 = tile * ROWS;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, half = lane >> 5;
-  const int r = r0 + wave * 32 + col;
-  const bool live = r < rows;
-  const Row me = row_of(a, h, min(r, rows - 1));
   const int len = kv_length(a, b);
-  const int lim = live ? kv_limit(a, len, me.query) : 0;
-  const int lim_lo = r0 + 128 > rows ? 0 : kv_limit(a, len, r0 / g.group);
-  const int lim_hi = kv_limit(a, len, (min(r0 + 128, rows) - 1) / g.group);
+  const int lim_lo = r0 + ROWS > rows ? 0 : kv_limit(a, len, r0 / g.group);
+  const int lim_hi = kv_limit(a, len, (min(r0 + ROWS, rows) - 1) / g.group);
   const int32_t* list = nullptr;
   const int reach = (lim_hi + 63) / 64;  // no block from here on, whatever a list says
   int count = reach;
@@ -517,272 +517,266 @@ __global__ __launch_bounds__(256, D == 128 ? (F32 ? 1 : 2) : (F32 ? 2 : 3)) void
   int parts, from, to;
   if (!part_of(a, count, split, parts, from, to)) return;
 
-  half8_t qh[NK], ql[NK];
-  float cq;
+  // Queries into LDS: 4 threads a row, every fourth 8 channels each. Operand f = 2 i + m,
+  // half hh has channels 16 (2 i + hh) + 8 m + 0..7: so that 16 consecutive codes of K in
+  // a lane are the operands of two matrix instructions.
   {
-    float top = 0.0f;
-    const IO* q = (const IO*)a.q.data + b * a.q.sb + (int64_t)me.query * a.q.st + me.head * a.q.sh + 8 * half;
+    const int r = tid >> 2 & (ROWS - 1), part = tid & 3;  // with 32 rows, each twice over
+    const Row me = row_of(a, h, min(r0 + r, rows - 1));
+    const IO* q = (const IO*)a.q.data + b * a.q.sb + (int64_t)me.query * a.q.st + me.head * a.q.sh;
+    float x[D / 32][8], top = 0.0f, up, down;
 #pragma unroll
-    for (int s = 0; s < NK; ++s) {
-      float x[8];
-      row8<IO>(q + 16 * s, x);
+    for (int s = 0; s < D / 32; ++s) {
+      row8<IO>(q + 32 * s + 8 * part, x[s]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[s][i]));
     }
-    top = max_halves(top);
-    float up, down;
+    top = group_max<4>(top);
     row_scale(top, up, down);
-    cq = down * (a.scale * kLog2e);
 #pragma unroll
-    for (int s = 0; s < NK; ++s) {
-      float x[8];
-      row8<IO>(q + 16 * s, x);
+    for (int s = 0; s < D / 32; ++s) {
+      half8_t hi, lo;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= up;
-      to_half<F32>(x, qh[s], ql[s]);
+      for (int i = 0; i < 8; ++i) x[s][i] *= up;
+      to_half<F32>(x[s], hi, lo);
+      // channels 32 s + 8 part: i = s, hh = part / 2, m = part % 2
+      sq[2 * s + part % 2][part / 2][r] = hi;
+      if constexpr (F32) sq[NK + 2 * s + part % 2][part / 2][r] = lo;
     }
+    if (part == 0) sml[0][r].x = down;
   }
-
-  u32x4 kr[UNITS], vr[UNITS];
-  const auto load_k = [&](int block, int u) {
-    const int unit = tid + 256 * u, p = unit & 63;
-    const int t = (p & ~12) | (p & 4) << 1 | (p & 8) >> 1;  // operand row -> token: bits 2 and 3 change places
-    kr[u] = *reinterpret_cast<const u32x4*>(g.k + kv_row(g, block, h) * (64 * D) + ((unit & ~63) | t) * 16);
-  };
-  const auto load_v = [&](int block, int u) {
-    vr[u] = *reinterpret_cast<const u32x4*>(g.v + kv_row(g, block, h) * (64 * D) + (tid + 256 * u) * 16);
-  };
-  // 8 of a unit's 16 codes, widened
-  const auto put_k = [&](int buf, int u, int part) {
-    const int unit = tid + 256 * u;
-    sk[buf][2 * (unit >> 6) + part][unit & 63] = codes8(kr[u][2 * part], kr[u][2 * part + 1]);
-  };
-  const auto put_v = [&](int buf, int u, int part) {
-    const int unit = tid + 256 * u;
-    sv[buf][2 * (unit / D) + part][unit % D] = codes8(vr[u][2 * part], vr[u][2 * part + 1]);
-  };
-  f32x16 o[ND];
+  __syncthreads();
+  float cq[U], m_run[U], l_run[U];
+  int lim[U];
 #pragma unroll
-  for (int d = 0; d < ND; ++d) o[d] = f32x16{};
-  float m_run = kLowest, l_run = 0.0f;
+  for (int u = 0; u < U; ++u) {
+    const int r = r0 + 32 * u + col;
+    cq[u] = sml[0][32 * u + col].x * (a.scale * kLog2e);
+    lim[u] = r < rows ? kv_limit(a, len, row_of(a, h, r).query) : 0;
+    m_run[u] = kLowest;
+    l_run[u] = 0.0f;
+  }
+  f32x16 o[U][ND];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[u][d] = f32x16{};
   int ev_cur = 0;
 
-  // S^T of the first or second half of the block in sk[buf]
-  const auto first_product = [&](f32x16& s, int buf, int u) {
-    s = f32x16{};
+  // Operand row -> token of a half block, so that result i of a lane is token 16 half + i.
+  const int token = (col & 3) | (col >> 3 & 1) << 2 | (col >> 4 & 1) << 3 | (col >> 2 & 1) << 4;
+  const uint32_t k_at = (uint32_t)(half * 64 + token) * 16u, v_at = (uint32_t)(half * D + col) * 16u;
+  u32x4 kr[NK / 2], vr[ND];
+  const auto load_k = [&](int block, int u) {  // a scalar base and the lane's offset
+    const uint8_t* k = g.k + kv_row(g, block, h) * (64 * D) + u * (32 * 16);
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const half8_t kf = sk[buf][2 * i + half][32 * u + col];
-      s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qh[i], s, 0, 0, 0);
-      if constexpr (F32) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, ql[i], s, 0, 0, 0);
-    }
+    for (int i = 0; i < NK / 2; ++i) kr[i] = *reinterpret_cast<const u32x4*>(k + (k_at + (uint32_t)i * (2 * 64 * 16)));
   };
-  const auto second_product = [&](const u32x4 (&ph)[2], const u32x4 (&pl)[2], int buf, int u) {
+  const auto load_v = [&](int block, int u) {
+    const uint8_t* v = g.v + kv_row(g, block, h) * (64 * D) + u * (2 * D * 16);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        const half8_t vf = sv[buf][4 * u + 2 * i + half][32 * d + col];
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, as_half8(ph[i]), o[d], 0, 0, 0);
-        if constexpr (F32) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, as_half8(pl[i]), o[d], 0, 0, 0);
-      }
-  };
-  // Masks of scores s (half u of block j), where the block may reach past a row's tokens.
-  const auto mask = [&](f32x16& s, int j, int u) {
-    if (j * 64 + 32 * u + 32 > lim_lo) {
-      const int left = lim - j * 64 - 32 * u - 8 * half;  // result i is token 16 (i / 8) + 8 half + i % 8
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (16 * (i / 8) + i % 8 >= left) s[i] = -INFINITY;
-    }
-  };
-  const auto rescale = [&](float f) {
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[d][i] *= f;
-  };
-  // After a step: probabilities in terms of an m that a row has left far behind do not
-  // fit f16. Their sum shows it (it is over kMost before any of them is over what f16
-  // holds), so no maximum is taken until then: m becomes the row's maximum, and the
-  // half's probabilities are computed again.
-  const auto settle = [&](const f32x16& s, u32x4 (&ph)[2], u32x4 (&pl)[2], float& sum, float ck, int delta) {
-    if (!__any(sum > kMost)) return;
-    float top = fmaxf(s[0], s[1]);
-#pragma unroll
-    for (int i = 2; i < 16; ++i) top = fmaxf(top, s[i]);
-    const float m_new = fmaxf(m_run, max_halves(top) * ck), alpha = exp2_fast(m_run - m_new);
-    l_run *= alpha;
-    m_run = m_new;
-    rescale(alpha);
-    const float off = kBias + (float)delta - m_run;
-    float p[16];
-    sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) p[i] = exp2_fast(fmaf(s[i], ck, off));
-#pragma unroll
-    for (int i = 0; i < 16; ++i) take_p<F32>(p, i, sum, ph, pl);
-  };
-  // One half block: the softmax of scores s into ph, pl; the second product of the
-  // half before (qh_, ql_: its p; vbuf, vu: its V); the first product of the half
-  // after (into sn, from kbuf, ku); where `put` says so, the staging of the next
-  // block; and at the end, after `between`, the first reads of the next step (nbuf,
-  // nu). Written out in the order in which it is to run, one matrix instruction at
-  // a time with its share of the rest, and kept so: left to itself the compiler puts
-  // all matrix instructions first, each waiting for its own LDS read, and the softmax
-  // after them.
-  constexpr int SLOTS = 2 * NK, AHEAD = 4, PER = 16 / SLOTS;
-  half8_t first[AHEAD];  // operands of a step's first matrix instructions, read in the step before
-  const auto step = [&](const f32x16& s, u32x4 (&ph)[2], u32x4 (&pl)[2], const u32x4 (&oh)[2],
-                        const u32x4 (&ol)[2], int vbuf, int vu, f32x16& sn, int kbuf, int ku, float ck, int delta,
-                        float& sum, int nbuf, int nu, auto put, auto between) {
-    static_assert(NK == 2 * ND, "as many matrix instructions for the first product as for the second");
-    const auto operand = [&](int i) {
-      return i < NK ? sk[kbuf][2 * i + half][32 * ku + col]
-                    : sv[vbuf][4 * vu + 2 * ((i - NK) / ND) + half][32 * ((i - NK) % ND) + col];
-    };
-    const float off = kBias + (float)delta - m_run;
-    half8_t in[SLOTS];
-    float p[16];
-    sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) in[i] = first[i];
-    sn = f32x16{};
-#pragma unroll
-    for (int i = 0; i < SLOTS; ++i) {
-      if (i + AHEAD < SLOTS) in[i + AHEAD] = operand(i + AHEAD);
-      if (i == SLOTS - 2) between();
-      if (i >= SLOTS - 2) {
-#pragma unroll
-        for (int n = (i - SLOTS + 2) * AHEAD / 2; n < (i - SLOTS + 3) * AHEAD / 2; ++n)
-          first[n] = sk[nbuf][2 * n + half][32 * nu + col];
-      }
-      // the first product first: its results are then there when the next step begins
-      if (i >= NK) {
-        const int k = i - NK;
-        o[k % ND] = __builtin_amdgcn_mfma_f32_32x32x16_f16(in[i], as_half8(oh[k / ND]), o[k % ND], 0, 0, 0);
-        if constexpr (F32) o[k % ND] = __builtin_amdgcn_mfma_f32_32x32x16_f16(in[i], as_half8(ol[k / ND]), o[k % ND], 0, 0, 0);
-      } else {
-        sn = __builtin_amdgcn_mfma_f32_32x32x16_f16(in[i], qh[i], sn, 0, 0, 0);
-        if constexpr (F32) sn = __builtin_amdgcn_mfma_f32_32x32x16_f16(in[i], ql[i], sn, 0, 0, 0);
-      }
-#pragma unroll
-      for (int e = i * PER; e < (i + 1) * PER; ++e) p[e] = exp2_fast(fmaf(s[e], ck, off));
-      if (i > 0) {
-#pragma unroll
-        for (int e = (i - 1) * PER; e < i * PER; ++e) take_p<F32>(p, e, sum, ph, pl);
-      }
-      if (i < SLOTS - 2) put(i);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int e = 16 - PER; e < 16; ++e) take_p<F32>(p, e, sum, ph, pl);
+    for (int d = 0; d < ND; ++d) vr[d] = *reinterpret_cast<const u32x4*>(v + (v_at + (uint32_t)d * (32 * 16)));
   };
 
-  Walk walk(g, list, b, h, from, to, 1, lane);
-  int block = -1, block1 = -1, block2 = -1, ev = 0, ev1 = 0, ev2 = 0;
-  float ks = 0.0f, ks1 = 0.0f, ks2 = 0.0f;
-  int j = walk.next(block, ks, ev);
-  if (j >= 0) {
-    f32x16 sa, sb;
-    u32x4 pa[2] = {}, pb[2] = {}, la[2] = {}, lb[2] = {};
-    // past the last block the registers are loaded with it again (not used), so that
-    // the steps have no branch
+  Walk walk(g, list, b, h, from + wave, to, 4, lane);
+  int block, slot, j = walk.next(block, slot);
+  if (j >= 0) load_k(block, 0);
+  while (j >= 0) {
+    float ks, factor;
+    int ev;
+    walk.scales(slot, ks, ev);
+    const int delta = enter_block(ev_cur, ev, factor);
+    const float back = pow2f(-delta);
+    if (factor != 1.0f) {
 #pragma unroll
-    for (int u = 0; u < UNITS; ++u) {
-      load_k(block, u);
-      load_v(block, u);
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[u][d][i] *= factor;
     }
+    int block_n = block;
+    const int j_n = walk.next(block_n, slot);
 #pragma unroll
-    for (int u = 0; u < UNITS; ++u) {
-      put_k(0, u, 0);
-      put_k(0, u, 1);
-    }
-    for (int i = tid; i < 8 * D; i += 256) sv[1][0][i] = half8_t{};  // the pending product of the first half: zero
-    block1 = block;
-    int j1 = walk.next(block1, ks1, ev1), buf = 0;
+    for (int hb = 0; hb < 2; ++hb) {  // half blocks of 32 tokens
+      load_v(block, hb);
+      // The products ahead of a wave in its softmax, so that the matrix units are fed first
+      // (bf16: image share 144 -> 141 us, video share 712 -> 700; fp32: no gain).
+      if constexpr (!F32) __builtin_amdgcn_s_setprio(1);
+      f32x16 s[U] = {};
+      constexpr int AHEAD = 1;
+      half8_t qf[NK][U];
 #pragma unroll
-    for (int u = 0; u < UNITS; ++u) load_k(block1, u);
-    __syncthreads();
-    first_product(sa, 0, 0);
+      for (int f = 0; f < AHEAD; ++f)
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) first[i] = sk[0][2 * i + half][32 + col];
-    while (true) {
-      const float ck = cq * ks;
-      float factor, sum;
-      const int delta = enter_block(ev_cur, ev, factor);
-      const float back = pow2f(-delta);
-      if (j * 64 + 64 > len) {
+        for (int u = 0; u < U; ++u) qf[f][u] = sq[f][half][32 * u + col];
 #pragma unroll
-        for (int u = 0; u < UNITS; ++u) vr[u] = keep_codes(vr[u], len - j * 64 - 16 * ((tid + 256 * u) / D));
-      }
-      // half 2 t. The buffers written here were last read before the previous block's
-      // barrier. A register's next load follows its last use: a whole block ahead.
-      block2 = block1;
-      const int j2 = j1 >= 0 ? walk.next(block2, ks2, ev2) : -1;
-      mask(sa, j, 0);
-      step(sa, pa, la, pb, lb, buf ^ 1, 1, sb, buf, 1, ck, delta, sum, buf ^ 1, 0, [&](int i) {
-        // half a unit in each of 4 * UNITS slots: V, then K; as late as the barrier allows
-        // where a block takes little time (D = 64: 824 us for the video share from slot 1,
-        // 770 from slot 2), since their loads were issued one block ago
-        constexpr int FROM = D == 64 ? 2 : 1;
-        static_assert(FROM + 4 * UNITS <= SLOTS - 2 || UNITS == 0, "staged before the barrier");
-        const int k = i - FROM, u = k / 2 % UNITS;
-        if (k < 0 || k >= 4 * UNITS) return;
-        if (k < 2 * UNITS) {
-          put_v(buf, u, k % 2);
-          if (k % 2) load_v(block1, u);
-        } else {
-          put_k(buf ^ 1, u, k % 2);
-          if (k % 2) load_k(block2, u);
+      for (int f = 0; f < NK; ++f) {
+        if (f + AHEAD < NK) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) qf[f + AHEAD][u] = sq[f + AHEAD][half][32 * u + col];
         }
-      }, [] { __syncthreads(); });
-      if (factor != 1.0f) rescale(factor);
-      settle(sa, pa, la, sum, ck, delta);
-      l_run = fmaf(sum, back, l_run);
-      // half 2 t + 1
-      mask(sb, j, 1);
-      step(sb, pb, lb, pa, la, buf, 0, sa, buf ^ 1, 0, ck, delta, sum, buf ^ 1, 1, [](int) {}, [] {});
-      settle(sb, pb, lb, sum, ck, delta);
-      l_run = fmaf(sum, back, l_run);
-      if (j1 < 0) break;
-      buf ^= 1;
-      j = j1; block = block1; ks = ks1; ev = ev1;
-      j1 = j2; block1 = block2; ks1 = ks2; ev1 = ev2;
+        const half8_t kf = codes8(kr[f / 2][2 * (f % 2)], kr[f / 2][2 * (f % 2) + 1]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[f][u], s[u], 0, 0, 0);
+          if constexpr (F32)
+            s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, sq[NK + f][half][32 * u + col], s[u], 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // K of the next half block, or past the end this block's again (not used)
+      load_k(hb == 0 ? block : block_n, 1 - hb);
+      if (j * 64 + 32 * hb + 32 > lim_lo) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          // by bits, not by comparisons, whose 32 results at once would spill scalars
+          const int left = min(max(lim[u] - j * 64 - 32 * hb - 16 * half, 0), 16);
+          const uint32_t seen = (1u << left) - 1u;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t on = (uint32_t)((int32_t)(seen << (31 - i)) >> 31);
+            s[u][i] = __uint_as_float((__float_as_uint(s[u][i]) & on) | (0xFF800000u & ~on));
+          }
+        }
+        if (j * 64 + 64 > len) {
+#pragma unroll
+          for (int d = 0; d < ND; ++d) vr[d] = keep_codes(vr[d], len - j * 64 - 32 * hb - 16 * half);
+        }
+      }
+      if constexpr (!F32) __builtin_amdgcn_s_setprio(0);
+      u32x4 ph[U][2], pl[U][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float ck = cq[u] * ks;
+        const auto weigh = [&](float& sum) {
+          const float off = kBias + (float)delta - m_run[u];
+          float p[16];
+          sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {  // four at a time, so that they take few registers
+#pragma unroll
+            for (int k = i; k < i + 4; ++k) p[k] = exp2_fast(fmaf(s[u][k], ck, off));
+#pragma unroll
+            for (int k = i; k < i + 4; ++k) take_p<F32>(p, k, sum, ph[u], pl[u]);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        };
+        float sum;
+        weigh(sum);
+        // Probabilities in terms of an m that a row has left far behind do not fit f16.
+        // Their sum shows it (it is over kMost before any of them is over what f16 holds),
+        // so no maximum is taken until then.
+        if (__any(sum > kMost)) {
+          float top = fmaxf(s[u][0], s[u][1]);
+#pragma unroll
+          for (int i = 2; i < 16; ++i) top = fmaxf(top, s[u][i]);
+          const float m_new = fmaxf(m_run[u], max_halves(top) * ck), alpha = exp2_fast(m_run[u] - m_new);
+          l_run[u] *= alpha;
+          m_run[u] = m_new;
+#pragma unroll
+          for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[u][d][i] *= alpha;
+          weigh(sum);
+        }
+        l_run[u] = fmaf(sum, back, l_run[u]);
+      }
+      if constexpr (!F32) __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const half8_t vf = codes8(vr[d][2 * m], vr[d][2 * m + 1]);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            o[u][d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, as_half8(ph[u][m]), o[u][d], 0, 0, 0);
+            if constexpr (F32)
+              o[u][d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, as_half8(pl[u][m]), o[u][d], 0, 0, 0);
+          }
+        }
     }
-    second_product(pb, lb, buf, 1);
+    j = j_n;
+    block = block_n;
   }
-  l_run += __shfl_xor(l_run, 32);
-  if (!live) return;
+
+  // join the waves: each scales to the common maximum of a row; 2 and 3 hand theirs to 0
+  // and 1, and 1 to 0's place, so the order of the sums is fixed
+  __syncthreads();  // the queries are read
+  {
+  // the thread's place again, from its number alone: kept through the loop it would spill
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int wave = tid >> 6, col = tid & 31, half = tid >> 5 & 1;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    l_run[u] += __shfl_xor(l_run[u], 32);
+    if (half == 0) sml[wave][32 * u + col] = make_float2(m_run[u], l_run[u]);
+  }
+  __syncthreads();
   const float unit = pow2f(ev_cur);
-  if (a.splits > 1 && split == 0 && half == 0) a.part_n[((int64_t)b * g.kv_heads + h) * rows + r] = parts;
-  if (parts > 1) {
-    const int64_t at = ((int64_t)split * g.batch + b) * g.kv_heads * rows + (int64_t)h * rows + r;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float m = kLowest;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, sml[w][32 * u + col].x);
+    const float f = exp2_fast(m_run[u] - m) * unit;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<f32x4*>(a.part + at * D + 32 * d + 8 * q + 4 * half) =
-            f32x4{o[d][4 * q], o[d][4 * q + 1], o[d][4 * q + 2], o[d][4 * q + 3]} * unit;
-    if (half == 0) a.part_ml[at] = make_float2(m_run, l_run);
-    return;
+      for (int i = 0; i < 16; ++i) o[u][d][i] *= f;
   }
-  const float inv = l_run > 0.0f ? unit / l_run : 0.0f;
-  IO* out = (IO*)a.out.data + b * a.out.sb + (int64_t)me.query * a.out.st + me.head * a.out.sh + 4 * half;
+  typedef float ORow[D + 4];
+  ORow* so = reinterpret_cast<ORow*>(shared);  // [2][ROWS] rows of outputs
+  const auto each = [&](int slab, auto&& what) {
 #pragma unroll
-  for (int d = 0; d < ND; ++d)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const f32x4 x = f32x4{o[d][4 * q], o[d][4 * q + 1], o[d][4 * q + 2], o[d][4 * q + 3]} * inv;
-      if constexpr (F32)
-        *reinterpret_cast<f32x4*>(out + 32 * d + 8 * q) = x;
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f32x4* at = reinterpret_cast<f32x4*>(&so[slab * ROWS + 32 * u + col][32 * d + 8 * q + 4 * half]);
+          what(at, f32x4{o[u][d][4 * q], o[u][d][4 * q + 1], o[u][d][4 * q + 2], o[u][d][4 * q + 3]});
+        }
+  };
+  if (wave >= 2) each(wave - 2, [](f32x4* at, f32x4 x) { *at = x; });
+  __syncthreads();
+  if (wave < 2) each(wave, [](f32x4* at, f32x4 x) { *at += x; });
+  __syncthreads();
+  // 4 threads a row
+  {
+    const int r = tid >> 2, part = tid & 3;
+    if (r >= ROWS || r0 + r >= rows) return;
+    float m = kLowest, l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, sml[w][r].x);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) l += sml[w][r].y * exp2_fast(sml[w][r].x - m);
+    const int64_t at = ((int64_t)b * g.kv_heads + h) * rows + r0 + r, all = (int64_t)g.batch * g.kv_heads * rows;
+    if (a.splits > 1 && split == 0 && part == 0) a.part_n[at] = parts;
+    const Row me = row_of(a, h, r0 + r);
+    const float inv = parts > 1 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+    IO* out = (IO*)a.out.data + b * a.out.sb + (int64_t)me.query * a.out.st + me.head * a.out.sh;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      const int d = 16 * s + 4 * part;
+      const f32x4 x = (*reinterpret_cast<const f32x4*>(&so[r][d]) + *reinterpret_cast<const f32x4*>(&so[ROWS + r][d])) * inv;
+      if (parts > 1)
+        *reinterpret_cast<f32x4*>(a.part + (split * all + at) * D + d) = x;
+      else if constexpr (F32)
+        *reinterpret_cast<f32x4*>(out + d) = x;
       else
-        *reinterpret_cast<u32x2*>(out + 32 * d + 8 * q) =
-            u32x2{bf16_rne(x.x) | bf16_rne(x.y) << 16, bf16_rne(x.z) | bf16_rne(x.w) << 16};
+        *reinterpret_cast<u32x2*>(out + d) = u32x2{bf16_rne(x.x) | bf16_rne(x.y) << 16, bf16_rne(x.z) | bf16_rne(x.w) << 16};
     }
-  if (a.lse && half == 0)
-    a.lse[((int64_t)b * a.queries + me.query) * g.q_heads + me.head] =
-        l_run > 0.0f ? (m_run - kBias + log2f(l_run)) * kLn2 : -INFINITY;
+    if (part == 0) {
+      if (parts > 1)
+        a.part_ml[split * all + at] = make_float2(m, l);
+      else if (a.lse)
+        a.lse[((int64_t)b * a.queries + me.query) * g.q_heads + me.head] =
+            l > 0.0f ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
+    }
+  }
+  }
 }
 
 // ------------------------------------------------------------------ joining splits
@@ -830,7 +824,7 @@ hipError_t run(const KvAttendArgs& a, bool few, hipStream_t s) {
     const dim3 grid((unsigned)(a.splits * groups), (unsigned)a.g.kv_heads, (unsigned)a.g.batch);
     kv_attend_few_kernel<D, F32><<<grid, 256, 0, s>>>(a);
   } else {
-    const int64_t grid = a.splits * ((rows + 127) / 128) * a.g.kv_heads * a.g.batch;
+    const int64_t grid = a.splits * ((rows + many_rows<D, F32>() - 1) / many_rows<D, F32>()) * a.g.kv_heads * a.g.batch;
     if (grid > INT32_MAX) return hipErrorInvalidValue;
     kv_attend_many_kernel<D, F32><<<(unsigned)grid, 256, 0, s>>>(a);
   }

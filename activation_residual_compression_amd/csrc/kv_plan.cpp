@@ -63,23 +63,24 @@ Way way_of(const rc_kv_plan* pl, int64_t queries, int64_t blocks, bool chosen, i
       }
     }
   } else {
-    // Blocks of threads that a CU holds at once (registers and LDS of the kernel).
-    const bool f32 = pl->dtype == RC_F32;
-    const int64_t at_once = 256 * (s.head_dim == 128 ? (f32 ? 1 : 2) : (f32 ? 2 : 3));
-    const int64_t base = heads * ceil_div(rows, 128);
-    // The time in steps of one block (about 1.8 us where the CUs are full): whole
-    // rounds of equal parts, or for causal rows, whose parts differ and are started
-    // longest first, the average and half the longest. Partial results cost a write
-    // and a read, and the launch that joins them.
+    // Blocks of threads that the CUs hold at once, and rows of each (the kernel's).
+    const int64_t at_once = 512, tile = s.head_dim == 128 && pl->dtype == RC_F32 ? 32 : 64;
+    const int64_t base = heads * ceil_div(rows, tile);
+    // The time in steps of four blocks, one a wave (about 3.6 us where the CUs are
+    // full), and 3 for the start and end of a block of threads: whole rounds of equal
+    // parts, or for causal rows, whose parts differ and are started longest first, the
+    // average and half the longest. Partial results cost a write and a read, and the
+    // launch that joins them.
     const bool causal = (pl->params.flags & RC_KV_CAUSAL) && !chosen;
     double best = 0.0;
     for (int64_t p = 1; p <= std::min({(int64_t)16, ceil_div(blocks, 8), std::max<int64_t>(most_rows / (heads * rows), 1)});
          ++p) {
-      const double len = (double)ceil_div(blocks, p);
-      const double mean = std::max(1.0, (double)blocks - (causal ? (double)std::min(queries / 128, blocks / 2) : 0.0));
+      const double len = (double)ceil_div(ceil_div(blocks, p), 4) + 1.0;
+      const double mean = (causal ? std::max(1.0, 0.25 * ((double)blocks - (double)std::min(queries / 128, blocks / 2)))
+                                  : 0.25 * (double)blocks) + 1.0 * (double)p;
       double cost = causal ? std::max((double)base * mean / at_once, len) + 0.5 * len
                            : (double)ceil_div(base * p, at_once) * len;
-      if (p > 1) cost += 3.0 + (double)(heads * rows * p) * (8.0 * s.head_dim) / 4e6 / 1.8;
+      if (p > 1) cost += 1.5 + (double)(heads * rows * p) * (8.0 * s.head_dim) / 4e6 / 3.6;
       if (p == 1 || cost < best) {
         best = cost;
         splits = p;
