@@ -65,7 +65,7 @@ struct KvAttendArgs {
 };
 hipError_t launch_kv_select(const KvAttendArgs& a, bool bf16, hipStream_t s);
 // few: the kernel for few rows (16 rows of a key head per block), else the one
-// for many (128 rows).
+// for many (64 rows, or 32 in fp32 at 128 channels).
 hipError_t launch_kv_attend(const KvAttendArgs& a, bool few, bool bf16, hipStream_t s);
 
 }  // namespace rc

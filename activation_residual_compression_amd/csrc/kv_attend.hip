@@ -23,7 +23,7 @@
 // one query only (its column), the softmax is in the lane, and the fp32 scores of
 // S^T are, rounded to f16 and with no exchange between lanes, the B operand of the
 // second product. For that, rows of the K operand are taken in an order that makes
-// the 8 results of a lane 8 consecutive tokens.
+// a lane's results runs of 8 (few rows) or 16 (many) consecutive tokens.
 #include <type_traits>
 
 #include "kv_device.hpp"
@@ -56,6 +56,11 @@ __device__ __forceinline__ void row_scale(float top, float& up, float& down) {
   up = pow2f(e);
   down = pow2f(-e);
 }
+
+// Factor of a row's scores in a block. Not zero, even where a row and a block of zeros
+// and a small scale of the scores meet: a masked score is -inf and has to stay it. What
+// is raised to 2^-126 belongs to scores under 2^-90, which leave p at 1 either way.
+__device__ __forceinline__ float factor_of(float row, float block) { return fmaxf(row * block, 0x1p-126f); }
 
 // Before a block of exponent ev: what goes into the exponent of p, and the factor
 // of the accumulators (1: nothing to do).
@@ -93,7 +98,8 @@ __device__ __forceinline__ int list_length(const int32_t* list, int keep, int re
 }
 
 // Takes in probability e of 16 (in order): the sum, and when it closes a pair, f16
-// (and for fp32 what that left). Pinned in place: see the step of the many-row kernel.
+// (and for fp32 what that left). Pinned in place, or the compiler gathers the sums and
+// conversions of all 16 behind the last exponential, which takes registers.
 template <bool F32>
 __device__ __forceinline__ void take_p(const float (&p)[16], int e, float& sum, u32x4 (&ph)[2], u32x4 (&pl)[2]) {
   sum += p[e];
@@ -201,7 +207,14 @@ struct Walk {
 // One block of threads: 16 rows of one key head, a part of the keys. Each of its
 // four waves reads blocks of its own straight into registers (a block's K and V
 // are 16 loads of 16 B a lane) and keeps its own running maximum and sum; the four
-// are joined in LDS, and the parts of the keys by the one that is done last. HBM bound: every code is read once for 16 rows.
+// are joined in LDS, and the parts of the keys by the one that is done last. HBM
+// bound: every code is read once for 16 rows. Three waves a SIMD without a prefetch
+// beat two with the next block's loads in flight on long sequences (716 us against
+// 739 for 64 of 32768 tokens). Measured with one query of four heads to a key head, 8
+// key heads of 128: 64 sequences of 32768 tokens 710 us (6.05 TB/s), 4 of 65536 95 us
+// (5.7), 32 ragged ones of up to 8192 68 us (4.5: the longest is the last to end); one
+// token over 333, 24 heads: 7.2 us, most of it the chain of dependent reads (length,
+// table, codes) and the launch.
 template <int D, bool F32>
 __global__ __launch_bounds__(256, F32 ? 2 : 3) void kv_attend_few_kernel(KvAttendArgs a) {
   constexpr int ND = D / 16, NQ = D / 64;
@@ -285,7 +298,7 @@ __global__ __launch_bounds__(256, F32 ? 2 : 3) void kv_attend_few_kernel(KvAtten
     float ks, factor;
     int ev;
     walk.scales(slot, ks, ev);
-    const float ck = cq * ks;
+    const float ck = factor_of(cq, ks);
     const int delta = enter_block(ev_cur, ev, factor);
 
     f32x4 s4[4];
@@ -437,28 +450,20 @@ __global__ __launch_bounds__(256, F32 ? 2 : 3) void kv_attend_few_kernel(KvAtten
 }
 
 // ------------------------------------------------------------------ many rows
-// Which part of the call a block of threads does. They go to the 8 XCDs in turn, so
-// where the load of the XCDs stays even, a key head's row tiles are given to one XCD,
-// whose L2 then holds its K and V: with a multiple of 8 key heads, head h to XCD h % 8
-// (every XCD gets the same share of every sequence, however long); with one sequence
-// whose rows all see the same, equal runs of the heads' tiles. Otherwise the tiles are
-// in order of length, the longest first, over all heads. Measured on 1152 queries over
-// 4608 tokens (2 x 24 heads of 128): 140 us, against 147 in plain order; the runs on
-// three ragged causal sequences of 4 key heads: 195 us against 115 in plain order.
+// Which part of the call a block of threads does. They go to the 8 XCDs in turn. With one
+// sequence whose rows all see the same, each XCD gets an equal run of the heads' tiles, so
+// that a head's K and V pass through one L2 (4444 queries over 17776 tokens, 30 heads of
+// 64: 695 us, 732 in plain order; over 70 chosen blocks each 220 and 228). Otherwise tiles
+// are in order of length, the longest first, over all heads: runs would leave XCDs with
+// the long sequences' tiles alone (three ragged causal sequences: 195 us in runs, 115 so),
+// and one head to one XCD gained nothing (two of 24 heads of 128: 139 us either way).
 struct Place {
   int b, h, split, tile;
 };
 __device__ __forceinline__ Place place_of(const KvAttendArgs& a, uint32_t w, uint32_t grid, int row_tiles) {
   const uint32_t per = (uint32_t)(row_tiles * a.splits), heads = (uint32_t)a.g.kv_heads;
   uint32_t in_head, b, h;
-  if (heads % 8 == 0) {
-    const uint32_t xcd = w & 7u;
-    w >>= 3;
-    in_head = w % per;
-    w /= per;
-    h = w % (heads / 8) * 8 + xcd;
-    b = w / (heads / 8);
-  } else if (!a.causal && a.g.batch == 1) {
+  if (!a.causal && a.g.batch == 1) {
     const uint32_t xcd = w & 7u;
     w = xcd * (grid >> 3) + min(xcd, grid & 7u) + (w >> 3);
     in_head = w % per;
@@ -485,9 +490,17 @@ __device__ __forceinline__ float max_halves(float x) {
 // read blocks of their own straight into registers, as in the kernel for few rows, so
 // the loop has no barrier and no LDS write, and the waves of a SIMD drift apart: one
 // does its softmax while another feeds the matrix units. All rows' queries are in LDS,
-// written once; an operand of K or V serves two groups of 32 rows
-// (one for fp32 at 128 channels, whose registers hold no more). The waves are joined
-// in LDS at the end.
+// written once; an operand of K or V serves two groups of 32 rows (one for fp32 at 128
+// channels, whose registers hold no more). The waves are joined in LDS at the end.
+//
+// Against 128 rows with K and V widened into LDS by all waves (two buffers, a barrier a
+// block): video share 764 -> 695 us, its block-selected form 250 -> 220, ragged causal
+// prompts 110 -> 95, image share 139 -> 139, in fp32 135 -> 141; there LDS writes cost
+// as much as the conversions. Bound by the vector units next to the matrix units: of
+// their cycles 63 % and 51 % at 128 channels, 87 % and 47 % at 64 (exponentials, sums and
+// the conversions of K and V, of which 64 rows share one). Measured: 1152 queries over
+// 4608 tokens, 2 x 24 heads of 128, 139 us (940 TFLOP/s); 4444 over 17776, 30 heads of
+// 64, 695 us (870).
 template <int D, bool F32>
 __global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) {
   constexpr int NK = D / 16, ND = D / 32, ROWS = many_rows<D, F32>(), U = ROWS / 32;
@@ -648,7 +661,7 @@ __global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) 
       u32x4 ph[U][2], pl[U][2];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const float ck = cq[u] * ks;
+        const float ck = factor_of(cq[u], ks);
         const auto weigh = [&](float& sum) {
           const float off = kBias + (float)delta - m_run[u];
           float p[16];
@@ -704,83 +717,84 @@ __global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) 
   // and 1, and 1 to 0's place, so the order of the sums is fixed
   __syncthreads();  // the queries are read
   {
-  // the thread's place again, from its number alone: kept through the loop it would spill
-  int tid = threadIdx.x;
-  asm volatile("" : "+v"(tid));
-  const int wave = tid >> 6, col = tid & 31, half = tid >> 5 & 1;
+    // the thread's place again, from its number alone: kept through the loop it would spill
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int wave = tid >> 6, col = tid & 31, half = tid >> 5 & 1;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    l_run[u] += __shfl_xor(l_run[u], 32);
-    if (half == 0) sml[wave][32 * u + col] = make_float2(m_run[u], l_run[u]);
-  }
-  __syncthreads();
-  const float unit = pow2f(ev_cur);
+    for (int u = 0; u < U; ++u) {
+      l_run[u] += __shfl_xor(l_run[u], 32);
+      if (half == 0) sml[wave][32 * u + col] = make_float2(m_run[u], l_run[u]);
+    }
+    __syncthreads();
+    const float unit = pow2f(ev_cur);
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    float m = kLowest;
+    for (int u = 0; u < U; ++u) {
+      float m = kLowest;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) m = fmaxf(m, sml[w][32 * u + col].x);
-    const float f = exp2_fast(m_run[u] - m) * unit;
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[u][d][i] *= f;
-  }
-  typedef float ORow[D + 4];
-  ORow* so = reinterpret_cast<ORow*>(shared);  // [2][ROWS] rows of outputs
-  const auto each = [&](int slab, auto&& what) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
+      for (int w = 0; w < 4; ++w) m = fmaxf(m, sml[w][32 * u + col].x);
+      const float f = exp2_fast(m_run[u] - m) * unit;
 #pragma unroll
       for (int d = 0; d < ND; ++d)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          f32x4* at = reinterpret_cast<f32x4*>(&so[slab * ROWS + 32 * u + col][32 * d + 8 * q + 4 * half]);
-          what(at, f32x4{o[u][d][4 * q], o[u][d][4 * q + 1], o[u][d][4 * q + 2], o[u][d][4 * q + 3]});
-        }
-  };
-  if (wave >= 2) each(wave - 2, [](f32x4* at, f32x4 x) { *at = x; });
-  __syncthreads();
-  if (wave < 2) each(wave, [](f32x4* at, f32x4 x) { *at += x; });
-  __syncthreads();
-  // 4 threads a row
-  {
-    const int r = tid >> 2, part = tid & 3;
-    if (r >= ROWS || r0 + r >= rows) return;
-    float m = kLowest, l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) m = fmaxf(m, sml[w][r].x);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) l += sml[w][r].y * exp2_fast(sml[w][r].x - m);
-    const int64_t at = ((int64_t)b * g.kv_heads + h) * rows + r0 + r, all = (int64_t)g.batch * g.kv_heads * rows;
-    if (a.splits > 1 && split == 0 && part == 0) a.part_n[at] = parts;
-    const Row me = row_of(a, h, r0 + r);
-    const float inv = parts > 1 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
-    IO* out = (IO*)a.out.data + b * a.out.sb + (int64_t)me.query * a.out.st + me.head * a.out.sh;
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      const int d = 16 * s + 4 * part;
-      const f32x4 x = (*reinterpret_cast<const f32x4*>(&so[r][d]) + *reinterpret_cast<const f32x4*>(&so[ROWS + r][d])) * inv;
-      if (parts > 1)
-        *reinterpret_cast<f32x4*>(a.part + (split * all + at) * D + d) = x;
-      else if constexpr (F32)
-        *reinterpret_cast<f32x4*>(out + d) = x;
-      else
-        *reinterpret_cast<u32x2*>(out + d) = u32x2{bf16_rne(x.x) | bf16_rne(x.y) << 16, bf16_rne(x.z) | bf16_rne(x.w) << 16};
+        for (int i = 0; i < 16; ++i) o[u][d][i] *= f;
     }
-    if (part == 0) {
-      if (parts > 1)
-        a.part_ml[split * all + at] = make_float2(m, l);
-      else if (a.lse)
-        a.lse[((int64_t)b * a.queries + me.query) * g.q_heads + me.head] =
-            l > 0.0f ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
+    typedef float ORow[D + 4];
+    ORow* so = reinterpret_cast<ORow*>(shared);  // [2][ROWS] rows of outputs
+    const auto each = [&](int slab, auto&& what) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            f32x4* at = reinterpret_cast<f32x4*>(&so[slab * ROWS + 32 * u + col][32 * d + 8 * q + 4 * half]);
+            what(at, f32x4{o[u][d][4 * q], o[u][d][4 * q + 1], o[u][d][4 * q + 2], o[u][d][4 * q + 3]});
+          }
+    };
+    if (wave >= 2) each(wave - 2, [](f32x4* at, f32x4 x) { *at = x; });
+    __syncthreads();
+    if (wave < 2) each(wave, [](f32x4* at, f32x4 x) { *at += x; });
+    __syncthreads();
+    // 4 threads a row
+    {
+      const int r = tid >> 2, part = tid & 3;
+      if (r >= ROWS || r0 + r >= rows) return;
+      float m = kLowest, l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) m = fmaxf(m, sml[w][r].x);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) l += sml[w][r].y * exp2_fast(sml[w][r].x - m);
+      const int64_t at = ((int64_t)b * g.kv_heads + h) * rows + r0 + r, all = (int64_t)g.batch * g.kv_heads * rows;
+      if (a.splits > 1 && split == 0 && part == 0) a.part_n[at] = parts;
+      const Row me = row_of(a, h, r0 + r);
+      const float inv = parts > 1 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+      IO* out = (IO*)a.out.data + b * a.out.sb + (int64_t)me.query * a.out.st + me.head * a.out.sh;
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        const int d = 16 * s + 4 * part;
+        const f32x4 x = (*reinterpret_cast<const f32x4*>(&so[r][d]) + *reinterpret_cast<const f32x4*>(&so[ROWS + r][d])) * inv;
+        if (parts > 1)
+          *reinterpret_cast<f32x4*>(a.part + (split * all + at) * D + d) = x;
+        else if constexpr (F32)
+          *reinterpret_cast<f32x4*>(out + d) = x;
+        else
+          *reinterpret_cast<u32x2*>(out + d) = u32x2{bf16_rne(x.x) | bf16_rne(x.y) << 16, bf16_rne(x.z) | bf16_rne(x.w) << 16};
+      }
+      if (part == 0) {
+        if (parts > 1)
+          a.part_ml[split * all + at] = make_float2(m, l);
+        else if (a.lse)
+          a.lse[((int64_t)b * a.queries + me.query) * g.q_heads + me.head] =
+              l > 0.0f ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
+      }
     }
-  }
   }
 }
 
 // ------------------------------------------------------------------ joining splits
-// D / 4 lanes a row: out = sum O_s 2^(m_s - m) / sum l_s 2^(m_s - m), parts in order.
+// D / 4 lanes a row: out = sum O_s 2^(m_s - m) / sum l_s 2^(m_s - m), parts in order. HBM
+// (or last-level cache) bound: 133 thousand rows of 64 in two parts, 20 us.
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void kv_attend_join_kernel(KvAttendArgs a) {
   typedef typename std::conditional<F32, float, uint16_t>::type IO;

@@ -3,8 +3,10 @@
 // One block of threads owns one 64-token block of one key head, of K or of V:
 // every scale is the maximum over exactly what one thread block holds, so a
 // single pass over the new values is enough (read once, 2 or 4 B an element; one
-// byte written). HBM bound for whole sequences; for single tokens the launch and
-// one dependent read (start, table, codes) are what it costs.
+// byte written). HBM bound for whole sequences: 4 x 4608 tokens of 24 x 128 bf16 68 to
+// 72 us (5.0 to 4.7 TB/s), 4444 of 30 x 64 fp32 15.8 us (5.4). For single tokens the
+// launch and the chain of reads (start, table, codes) are what it costs: 16 sequences,
+// 8 heads of 128, 5.9 us.
 #include "kv_device.hpp"
 
 namespace rc {

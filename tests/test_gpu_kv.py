@@ -221,6 +221,23 @@ def test_attend_block_scales_far_apart(nq):
     check_attend(cache, to_gpu(cache), {}, np.arange(8, dtype=np.int32)[None], [500], q32, q, False)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq", [3, 129])
+def test_attend_zero_rows_and_blocks_at_a_small_scale(dtype, nq):
+    """Masked tokens weigh nothing where the factor of the scores underflows: rows of zeros,
+    blocks of zeros at the smallest scale, and a scale of 1e-12."""
+    rng = np.random.default_rng(nq)
+    cache = filled(rng, 4, 1, 64, k_exponents=(-40, -40))
+    cache.k[1:] = 0
+    kv = to_gpu(cache)
+    q32, q = values(rng, (1, nq, 1, 64), dtype)
+    q32[:, ::2] = 0
+    q[:, ::2] = 0
+    for causal in (True, False):
+        say("[gpu] zero rows %s %d causal %s" % (dtype, nq, causal))
+        check_attend(cache, kv, dict(scale=1e-12), np.array([[1, 0, 3, 2]], np.int32), [230], q32, q, causal)
+
+
 @pytest.mark.parametrize("nq", [2, 140])
 def test_attend_strided_queries_and_outputs(nq):
     rng = np.random.default_rng(nq)
