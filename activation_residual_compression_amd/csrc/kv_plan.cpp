@@ -38,10 +38,19 @@ Way way_of(const rc_kv_plan* pl, int64_t queries, int64_t blocks, bool chosen, i
   const int64_t group = s.q_heads / s.kv_heads, rows = queries * group;
   const bool own_lists = chosen && pl->params.q_tile == 1;
   Way w;
-  w.few = own_lists || rows <= 64;
   const int64_t heads = (int64_t)s.batch * s.kv_heads;
   int64_t splits = 1;
   blocks = std::max<int64_t>(blocks, 1);
+  // Up to 64 rows, the kernel for few reads (and converts) K and V once more for each
+  // 16 rows after the first, and the kernel for many has a larger tile than rows and a
+  // second launch for the join. Measured in us, few and many, bf16, 8 key heads of 128,
+  // rows 32 and 64: one sequence of 2000 tokens (4 MB) 12 and 17, 12 and 17; 32 of 4096
+  // (268 MB) 97 and 72, 175 and 81: equal at about 45 and 12 MB. In fp32 with 64
+  // channels, where the tile is 64 rows of twice the products, 32 rows over 134 MB are
+  // 44 and 61, and 48 rows 65 and 67.
+  const int64_t again = (ceil_div(std::min<int64_t>(rows, 64), 16) - 1) * heads * blocks * 128 * s.head_dim;
+  w.few = own_lists || rows <= 16 ||
+          (rows <= 64 && (again <= (int64_t)32 << 20 || (rows <= 32 && s.head_dim == 64 && pl->dtype == RC_F32)));
   if (w.few) {
     const int64_t base = heads * (own_lists ? queries * ceil_div(group, 16) : ceil_div(rows, 16));
     // The time in microseconds: the bytes at 5.8 TB/s, or the waves' blocks one after
@@ -264,8 +273,8 @@ rc_status_t rc_kv_store(rc_kv_plan_t pl, hipStream_t stream, const rc_kv_cache_t
   a.g = geometry(pl, cache, table);
   a.start = start;
   a.count = count;
-  a.tokens = tokens;
-  a.once = (int64_t)s.batch * tokens * s.kv_heads * s.head_dim *
+  a.tokens = (int)std::min<int64_t>(tokens, (int64_t)RC_KV_BLOCK * s.seq_blocks);  // later ones are dropped anyway
+  a.once = (int64_t)s.batch * a.tokens * s.kv_heads * s.head_dim *
                ((k->dtype == RC_BF16 ? 2 : 4) + (v->dtype == RC_BF16 ? 2 : 4)) > (int64_t)128 << 20;
   return rc::launch_kv_store(a, k->dtype == RC_BF16, v->dtype == RC_BF16, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
 }
