@@ -499,8 +499,8 @@ __device__ __forceinline__ float max_halves(float x) {
 // as much as the conversions. Bound by the vector units next to the matrix units: of
 // their cycles 63 % and 51 % at 128 channels, 87 % and 47 % at 64 (exponentials, sums and
 // the conversions of K and V, of which 64 rows share one). Measured: 1152 queries over
-// 4608 tokens, 2 x 24 heads of 128, 139 us (940 TFLOP/s); 4444 over 17776, 30 heads of
-// 64, 695 us (870).
+// 4608 tokens, 2 x 24 heads of 128, 139 to 144 us on different cards (up to 940 TFLOP/s);
+// 4444 over 17776, 30 heads of 64, 695 to 723 us (up to 870).
 template <int D, bool F32>
 __global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) {
   constexpr int NK = D / 16, ND = D / 32, ROWS = many_rows<D, F32>(), U = ROWS / 32;

@@ -247,7 +247,8 @@ rc_status_t rc_kv_plan_create(rc_kv_shape_t shape, rc_dtype_t dtype, const rc_kv
     }
     pl->ws_bytes = parts + counts;
     pl->arrived = reinterpret_cast<uint32_t*>(static_cast<char*>(pl->ws) + parts);
-    if (hipMemset(pl->arrived, 0, counts) != hipSuccess) {
+    // done before the first call, which may be on a stream that does not wait for this one
+    if (hipMemset(pl->arrived, 0, counts) != hipSuccess || hipStreamSynchronize(nullptr) != hipSuccess) {
       (void)hipFree(pl->ws);
       delete pl;
       return RC_ERR_HIP;
