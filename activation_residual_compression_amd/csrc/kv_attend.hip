@@ -117,6 +117,11 @@ __device__ __forceinline__ void take_p(const float (&p)[16], int e, float& sum, 
 }
 __device__ __forceinline__ half8_t as_half8(u32x4 x) { return __builtin_bit_cast(half8_t, x); }
 
+// What a row's outputs are multiplied by at the end, and its log-sum-exp. Only a sum of
+// zero is a row that sees nothing: one that is NaN stays NaN.
+__device__ __forceinline__ float inverse_of(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m - kBias + log2f(l)) * kLn2; }
+
 // The part of a group's n blocks that this block of threads reads; parts: of how many.
 __device__ __forceinline__ bool part_of(const KvAttendArgs& a, int n, int split, int& parts, int& from, int& to) {
   parts = min(max((n + a.chunk - 1) / a.chunk, 1), a.splits);
@@ -434,7 +439,7 @@ __global__ __launch_bounds__(256, F32 ? 2 : 3) void kv_attend_few_kernel(KvAtten
   }
   if (!mine) return;
   const Row to_row = row_of(a, h, r0 + rr);
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = inverse_of(l);
   IO* out = (IO*)a.out.data + b * a.out.sb + (int64_t)to_row.query * a.out.st + to_row.head * a.out.sh + d0;
 #pragma unroll
   for (int i = 0; i < ND / 4; ++i) {
@@ -445,8 +450,7 @@ __global__ __launch_bounds__(256, F32 ? 2 : 3) void kv_attend_few_kernel(KvAtten
       *reinterpret_cast<u32x2*>(out + 4 * i) = u32x2{bf16_rne(y.x) | bf16_rne(y.y) << 16, bf16_rne(y.z) | bf16_rne(y.w) << 16};
   }
   if (a.lse && (tid & 15) == 0)
-    a.lse[((int64_t)b * a.queries + to_row.query) * g.q_heads + to_row.head] =
-        l > 0.0f ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
+    a.lse[((int64_t)b * a.queries + to_row.query) * g.q_heads + to_row.head] = lse_of(m, l);
 }
 
 // ------------------------------------------------------------------ many rows
@@ -768,7 +772,7 @@ __global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) 
       const int64_t at = ((int64_t)b * g.kv_heads + h) * rows + r0 + r, all = (int64_t)g.batch * g.kv_heads * rows;
       if (a.splits > 1 && split == 0 && part == 0) a.part_n[at] = parts;
       const Row me = row_of(a, h, r0 + r);
-      const float inv = parts > 1 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+      const float inv = parts > 1 ? 1.0f : inverse_of(l);
       IO* out = (IO*)a.out.data + b * a.out.sb + (int64_t)me.query * a.out.st + me.head * a.out.sh;
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
@@ -786,7 +790,7 @@ __global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) 
           a.part_ml[split * all + at] = make_float2(m, l);
         else if (a.lse)
           a.lse[((int64_t)b * a.queries + me.query) * g.q_heads + me.head] =
-              l > 0.0f ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
+              lse_of(m, l);
       }
     }
   }
@@ -819,15 +823,14 @@ __global__ __launch_bounds__(256) void kv_attend_join_kernel(KvAttendArgs a) {
   }
   const int r = (int)(at % rows), h = (int)(at / rows % g.kv_heads), b = (int)(at / rows / g.kv_heads);
   const Row me = row_of(a, h, r);
-  x *= l > 0.0f ? 1.0f / l : 0.0f;
+  x *= inverse_of(l);
   IO* out = (IO*)a.out.data + b * a.out.sb + (int64_t)me.query * a.out.st + me.head * a.out.sh + d0;
   if constexpr (F32)
     *reinterpret_cast<f32x4*>(out) = x;
   else
     *reinterpret_cast<u32x2*>(out) = u32x2{bf16_rne(x.x) | bf16_rne(x.y) << 16, bf16_rne(x.z) | bf16_rne(x.w) << 16};
   if (a.lse && d0 == 0)
-    a.lse[((int64_t)b * a.queries + me.query) * g.q_heads + me.head] =
-        l > 0.0f ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
+    a.lse[((int64_t)b * a.queries + me.query) * g.q_heads + me.head] = lse_of(m, l);
 }
 
 template <int D, bool F32>

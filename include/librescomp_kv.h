@@ -146,11 +146,12 @@ rc_status_t rc_kv_select(rc_kv_plan_t plan, hipStream_t stream, const rc_kv_cach
  * out: [batch][queries][q_heads][head_dim] in the plan's dtype.
  * lse (NULL, or fp32 [batch][queries][q_heads]): the natural logarithm of the sum
  * of the exponentials, to join this result with attention over other tokens. A
- * query that sees no token gets 0 and -infinity.
- * NaN: a key's reaches the queries that see it. A value's reaches those too and, with
- * RC_KV_CAUSAL, may reach earlier queries of the call for which its block is read
- * (its weight there is zero, and zero times NaN is NaN). What a block holds after
- * its sequence's end reaches no one. */
+ * query that sees no token, or whose scores are all -infinity, gets 0 and -infinity.
+ * NaN: a key's makes the outputs and the lse of the queries that see it NaN; a query's,
+ * or scores of +infinity, its own. A value's reaches the outputs, not the lse, of the
+ * queries that see it and, with RC_KV_CAUSAL, may reach the outputs of earlier queries of
+ * the call for which its block is read (its weight there is zero, and zero times NaN is
+ * NaN). What a block holds after its sequence's end reaches no one. */
 rc_status_t rc_kv_attend(rc_kv_plan_t plan, hipStream_t stream, const rc_kv_cache_t* cache,
                          const int32_t* table, const int32_t* kv_len, int64_t max_len, int queries,
                          const rc_kv_view_t* q, const int32_t* blocks, const rc_kv_view_t* out, float* lse);

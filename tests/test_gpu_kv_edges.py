@@ -1,0 +1,77 @@
+"""The 8-bit key/value cache at its edges, against 64 bits (kv_dense; the bounds are the
+ones that test_gpu_kv derives)."""
+import numpy as np
+import pytest
+import torch
+
+import kv_dense
+import kv_oracle as ko
+from gpu_harness import DEV, say
+from activation_residual_compression_amd import librescomp as rc
+from test_gpu_kv import filled, ints, to_gpu, values
+
+pytestmark = pytest.mark.gpu
+
+
+def as_query(x, dtype):
+    """fp32 array -> (what the library sees, device tensor)."""
+    t = torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    return t.float().numpy(), t.to(DEV)
+
+
+def new_plan(cache, table, q, causal, **kw):
+    B, nq, qh, d = q.shape
+    return rc.KvPlan(batch=B, q_heads=qh, kv_heads=cache.k_scale.shape[1], head_dim=d, pool_blocks=cache.k_scale.shape[0],
+                     seq_blocks=table.shape[1], dtype="f32" if q.dtype == torch.float32 else "bf16", causal=causal,
+                     **{"max_queries": nq, **kw})
+
+
+def run(plan, kv, table, lens, q, blocks=None, max_len=0):
+    out = torch.full(q.shape, 77.0, dtype=q.dtype, device=DEV)
+    lse = torch.full(q.shape[:3], 77.0, device=DEV)
+    plan.attend(kv, ints(lens), q, out, lse, table=ints(table), blocks=blocks, max_len=max_len)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+def check(cache, table, lens, q32, causal, out, lse, lists=None, q_tile=0, scale=0.0, which=None, max_len=0):
+    """What run returned, for all sequences or those of `which`."""
+    d = q32.shape[3]
+    for b in range(q32.shape[0]) if which is None else which:
+        n = max(0, min(int(lens[b]), 64 * table.shape[1], max_len or 1 << 40))
+        ref = kv_dense.attend(cache, table[b], n, q32[b].astype(np.float64), causal,
+                              float(np.float32(scale)) or 1.0 / np.float64(np.sqrt(np.float32(d))),
+                              None if lists is None else lists[b], q_tile)
+        kv_dense.check(out[b].double().cpu().numpy(), lse[b].double().cpu().numpy(), ref, n, d, out.dtype == torch.float32)
+
+
+# ------------------------------------------------------------------ not finite
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("nq,n", [(3, 200), (3, 64 * 40 + 13), (130, 300), (130, 64 * 40 + 13)])
+@pytest.mark.parametrize("what", ["key", "value", "query", "infinite query"])
+def test_nan_reaches_the_queries_that_see_it(dtype, dim, nq, n, what):
+    """In the output and in its log-sum-exp (a value's in the output alone), and no other
+    query: one part of the keys and several, few rows and many."""
+    rng = np.random.default_rng(nq + n)
+    nb = -(-n // 64)
+    cache = filled(rng, nb, 2, dim)
+    table = rng.permutation(nb).reshape(1, nb).astype(np.int32)
+    q32, _ = values(rng, (1, nq, 4, dim), dtype, 0.7)
+    at = n - nq // 2 - 1                                        # with a causal mask half of the queries see it
+    kc, vc = (c(table[0, at // 64], 0).copy() for c in (cache.k_codes, cache.v_codes))
+    if what == "key":
+        kc[at % 64, 7] = 0xFF
+    elif what == "value":
+        vc[at % 64, 3], vc[at % 64, dim - 1] = 0xFF, 0x7F
+    else:
+        q32[0, 1, 2, 5] = np.nan if what == "query" else np.inf
+    cache.put(table[0, at // 64], 0, kc, vc)
+    kv = to_gpu(cache)
+    q32, q = as_query(q32, dtype)
+    for causal in (True, False):
+        say("[gpu] %s nan %s %d queries %d over %d causal %d" % (what, dtype, dim, nq, n, causal))
+        with new_plan(cache, table, q, causal) as plan:
+            out, lse = run(plan, kv, table, [n], q)
+        check(cache, table, [n], q32, causal, out, lse)
+
