@@ -447,7 +447,7 @@ __global__ __launch_bounds__(256, F32 ? 2 : 3) void kv_attend_few_kernel(KvAtten
     if constexpr (F32)
       *reinterpret_cast<f32x4*>(out + 4 * i) = y;
     else
-      *reinterpret_cast<u32x2*>(out + 4 * i) = u32x2{bf16_rne(y.x) | bf16_rne(y.y) << 16, bf16_rne(y.z) | bf16_rne(y.w) << 16};
+      *reinterpret_cast<u32x2*>(out + 4 * i) = u32x2{bf16_pair(y.x, y.y), bf16_pair(y.z, y.w)};
   }
   if (a.lse && (tid & 15) == 0)
     a.lse[((int64_t)b * a.queries + to_row.query) * g.q_heads + to_row.head] = lse_of(m, l);
@@ -783,7 +783,7 @@ __global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) 
         else if constexpr (F32)
           *reinterpret_cast<f32x4*>(out + d) = x;
         else
-          *reinterpret_cast<u32x2*>(out + d) = u32x2{bf16_rne(x.x) | bf16_rne(x.y) << 16, bf16_rne(x.z) | bf16_rne(x.w) << 16};
+          *reinterpret_cast<u32x2*>(out + d) = u32x2{bf16_pair(x.x, x.y), bf16_pair(x.z, x.w)};
       }
       if (part == 0) {
         if (parts > 1)
@@ -828,7 +828,7 @@ __global__ __launch_bounds__(256) void kv_attend_join_kernel(KvAttendArgs a) {
   if constexpr (F32)
     *reinterpret_cast<f32x4*>(out) = x;
   else
-    *reinterpret_cast<u32x2*>(out) = u32x2{bf16_rne(x.x) | bf16_rne(x.y) << 16, bf16_rne(x.z) | bf16_rne(x.w) << 16};
+    *reinterpret_cast<u32x2*>(out) = u32x2{bf16_pair(x.x, x.y), bf16_pair(x.z, x.w)};
   if (a.lse && d0 == 0)
     a.lse[((int64_t)b * a.queries + me.query) * g.q_heads + me.head] = lse_of(m, l);
 }

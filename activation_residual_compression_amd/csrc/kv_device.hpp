@@ -47,6 +47,14 @@ __device__ __forceinline__ void row8(const IN* p, float (&x)[8]) {
   for (int i = 0; i < 8; ++i) x[i] = t.v[i];
 }
 
+// Two outputs as bf16, rounded to nearest even; a NaN of any payload stays one (bf16_rne is
+// for finite values, and would carry a full payload into the sign).
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
 // Four e4m3 codes -> four f16 (exact: every e4m3 value is a normal f16).
 __device__ __forceinline__ void codes4(uint32_t c, half2_t& lo, half2_t& hi) {
   lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.0f, false);

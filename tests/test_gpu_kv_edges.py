@@ -75,3 +75,19 @@ def test_nan_reaches_the_queries_that_see_it(dtype, dim, nq, n, what):
             out, lse = run(plan, kv, table, [n], q)
         check(cache, table, [n], q32, causal, out, lse)
 
+
+@pytest.mark.parametrize("nq,n", [(3, 200), (3, 64 * 40 + 13), (130, 300), (130, 64 * 40 + 13)])
+@pytest.mark.parametrize("bits", [0x7F81, 0x7FFF, -1, -127])
+def test_nan_of_any_payload_stays_nan_in_bf16(nq, n, bits):
+    """bf16 queries that hold a NaN of any sign and payload (int16 bits)."""
+    rng = np.random.default_rng(nq + n)
+    nb = -(-n // 64)
+    cache = filled(rng, nb, 2, 64)
+    table = rng.permutation(nb).reshape(1, nb).astype(np.int32)
+    q32, q = values(rng, (1, nq, 4, 64), "bf16", 0.7)
+    q.view(torch.int16)[0, 1, 2] = bits
+    q32[0, 1, 2] = np.nan
+    say("[gpu] nan bits %x, %d queries over %d" % (bits & 0xFFFF, nq, n))
+    with new_plan(cache, table, q, True) as plan:
+        out, lse = run(plan, to_gpu(cache), table, [n], q)
+    check(cache, table, [n], q32, True, out, lse)
