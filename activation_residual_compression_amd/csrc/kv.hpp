@@ -52,7 +52,7 @@ struct KvAttendArgs {
   int max_len;            // bound of kv_len, at most 64 * seq_blocks
   int queries, causal;
   int q_tile, keep, tiles;
-  float scale;            // of the scores
+  float scale;            // of the scores, in base 2: the plan's times log2(e)
   // Split over the keys: a group of rows that reads n blocks does so in
   // ceil(n / chunk) parts of equal length, at most `splits`, each by a block of
   // threads of its own. With one part it writes the outputs; with more, each writes

@@ -31,7 +31,7 @@
 namespace rc {
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kBias = 7.0f, kMost = 0x1p15f;  // f16 holds 2^15
 constexpr int kEvUp = 2, kEvDown = 8;
 constexpr float kLowest = -3.402823466e38f;
@@ -49,18 +49,22 @@ __device__ __forceinline__ Row row_of(const KvAttendArgs& a, int h, int r) {
   return {r / a.g.group, h * a.g.group + r % a.g.group};
 }
 
-// Power of two that brings a row's largest value into [2^14, 2^15), and its inverse.
-__device__ __forceinline__ void row_scale(float top, float& up, float& down) {
+// Power of two that brings a row's largest value into [2^14, 2^15), and the exponent of
+// its inverse. Rows under 2^-113 (2^127 is the largest factor) stay below 2^14.
+__device__ __forceinline__ float row_scale(float top, int& down) {
   const int ex = (int)(__float_as_uint(top) >> 23 & 255);  // biased; 0: zero or subnormal
-  const int e = min(max(141 - ex, -100), 100);
-  up = pow2f(e);
-  down = pow2f(-e);
+  down = max(ex - 141, -127);
+  return pow2f(-down);
 }
 
-// Factor of a row's scores in a block. Not zero, even where a row and a block of zeros
-// and a small scale of the scores meet: a masked score is -inf and has to stay it. What
-// is raised to 2^-126 belongs to scores under 2^-90, which leave p at 1 either way.
-__device__ __forceinline__ float factor_of(float row, float block) { return fmaxf(row * block, 0x1p-126f); }
+// Factor of a row's scores in a block: scale * 2^e, e the sum of the row's exponent and of
+// the block's (-167 to 158), so that no product on the way leaves fp32 where the factor is
+// in it. Not zero, even where a row and a block of zeros and a small scale meet: a masked
+// score is -inf and has to stay it. What is raised to 2^-126 belongs to scores under 2^-90,
+// which leave p at 1 either way. Not infinite, so that scores of zero stay it too.
+__device__ __forceinline__ float factor_of(float scale, int e) {
+  return fminf(fmaxf(ldexpf(scale, e), 0x1p-126f), -kLowest);
+}
 
 // Before a block of exponent ev: what goes into the exponent of p, and the factor
 // of the accumulators (1: nothing to do).
@@ -195,16 +199,10 @@ struct Walk {
     return __builtin_amdgcn_readlane((int)lane_what, at) & 0xFFFF;
   }
   // Exponents of the scales of the block that next() found, before the next call of it.
-  __device__ __forceinline__ void scales(int at, float& ks, int& ev) const {
+  __device__ __forceinline__ void scales(int at, int& ks, int& ev) const {
     const uint32_t what = (uint32_t)__builtin_amdgcn_readlane((int)lane_what, at);
-    ks = pow2f((int)(what >> 16 & 255u) - 64);
+    ks = (int)(what >> 16 & 255u) - 64;
     ev = (int)(what >> 24) - 64;
-  }
-  __device__ __forceinline__ int next(int& block, float& ks, int& ev) {
-    int at;
-    const int j = next(block, at);
-    if (j >= 0) scales(at, ks, ev);
-    return j;
   }
 };
 
@@ -253,7 +251,7 @@ __global__ __launch_bounds__(256, F32 ? 2 : 3) void kv_attend_few_kernel(KvAtten
   if (!part_of(a, count, split, parts, from, to)) return;
 
   half8_t qh[NQ][2], ql[NQ][2];
-  float cq;
+  int eq;  // the row's scores are 2^eq times the products
   {
     float x[NQ][2][8], top = 0.0f;
 #pragma unroll
@@ -267,9 +265,7 @@ __global__ __launch_bounds__(256, F32 ? 2 : 3) void kv_attend_few_kernel(KvAtten
       }
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
-    float up, down;
-    row_scale(top, up, down);
-    cq = down * (a.scale * kLog2e);
+    const float up = row_scale(top, eq);
 #pragma unroll
     for (int s = 0; s < NQ; ++s)
 #pragma unroll
@@ -300,10 +296,10 @@ __global__ __launch_bounds__(256, F32 ? 2 : 3) void kv_attend_few_kernel(KvAtten
         k[t][s] = *reinterpret_cast<const u32x4*>(kb + ((4 * s + quad) * 64 + 16 * (col >> 2) + 4 * t + (col & 3)) * 16);
 #pragma unroll
     for (int d = 0; d < ND; ++d) v[d] = *reinterpret_cast<const u32x4*>(vb + (quad * D + 16 * d + col) * 16);
-    float ks, factor;
-    int ev;
+    float factor;
+    int ks, ev;
     walk.scales(slot, ks, ev);
-    const float ck = factor_of(cq, ks);
+    const float ck = factor_of(a.scale, eq + ks);
     const int delta = enter_block(ev_cur, ev, factor);
 
     f32x4 s4[4];
@@ -506,7 +502,7 @@ __device__ __forceinline__ float max_halves(float x) {
 // 4608 tokens, 2 x 24 heads of 128, 139 to 144 us on different cards (up to 940 TFLOP/s);
 // 4444 over 17776, 30 heads of 64, 695 to 723 us (up to 870).
 template <int D, bool F32>
-__global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) {
+__global__ __launch_bounds__(256, D == 128 && !F32 ? 2 : 3) void kv_attend_many_kernel(KvAttendArgs a) {
   constexpr int NK = D / 16, ND = D / 32, ROWS = many_rows<D, F32>(), U = ROWS / 32;
   typedef typename std::conditional<F32, float, uint16_t>::type IO;
   constexpr int QBYTES = (F32 ? 2 : 1) * NK * 2 * ROWS * 16, OBYTES = 2 * ROWS * (D + 4) * 4;
@@ -541,7 +537,7 @@ __global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) 
     const int r = tid >> 2 & (ROWS - 1), part = tid & 3;  // with 32 rows, each twice over
     const Row me = row_of(a, h, min(r0 + r, rows - 1));
     const IO* q = (const IO*)a.q.data + b * a.q.sb + (int64_t)me.query * a.q.st + me.head * a.q.sh;
-    float x[D / 32][8], top = 0.0f, up, down;
+    float x[D / 32][8], top = 0.0f;
 #pragma unroll
     for (int s = 0; s < D / 32; ++s) {
       row8<IO>(q + 32 * s + 8 * part, x[s]);
@@ -549,7 +545,8 @@ __global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) 
       for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[s][i]));
     }
     top = group_max<4>(top);
-    row_scale(top, up, down);
+    int down;
+    const float up = row_scale(top, down);
 #pragma unroll
     for (int s = 0; s < D / 32; ++s) {
       half8_t hi, lo;
@@ -560,15 +557,15 @@ __global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) 
       sq[2 * s + part % 2][part / 2][r] = hi;
       if constexpr (F32) sq[NK + 2 * s + part % 2][part / 2][r] = lo;
     }
-    if (part == 0) sml[0][r].x = down;
+    if (part == 0) sml[0][r].x = (float)down;
   }
   __syncthreads();
-  float cq[U], m_run[U], l_run[U];
-  int lim[U];
+  float m_run[U], l_run[U];
+  int eq[U], lim[U];  // a row's scores are 2^eq times the products
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int r = r0 + 32 * u + col;
-    cq[u] = sml[0][32 * u + col].x * (a.scale * kLog2e);
+    eq[u] = (int)sml[0][32 * u + col].x;
     lim[u] = r < rows ? kv_limit(a, len, row_of(a, h, r).query) : 0;
     m_run[u] = kLowest;
     l_run[u] = 0.0f;
@@ -599,8 +596,8 @@ __global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) 
   int block, slot, j = walk.next(block, slot);
   if (j >= 0) load_k(block, 0);
   while (j >= 0) {
-    float ks, factor;
-    int ev;
+    float factor;
+    int ks, ev;
     walk.scales(slot, ks, ev);
     const int delta = enter_block(ev_cur, ev, factor);
     const float back = pow2f(-delta);
@@ -665,7 +662,7 @@ __global__ __launch_bounds__(256, 2) void kv_attend_many_kernel(KvAttendArgs a) 
       u32x4 ph[U][2], pl[U][2];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const float ck = factor_of(cq[u], ks);
+        const float ck = factor_of(a.scale, eq[u] + ks);
         const auto weigh = [&](float& sum) {
           const float off = kBias + (float)delta - m_run[u];
           float p[16];

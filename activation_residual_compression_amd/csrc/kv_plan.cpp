@@ -209,7 +209,8 @@ rc_status_t prepare(rc_kv_plan* pl, const rc_kv_cache_t* cache, const int32_t* t
   a->q_tile = pl->params.q_tile;
   a->keep = pl->params.keep_blocks;
   a->tiles = a->q_tile ? (int)ceil_div(queries, a->q_tile) : 0;
-  a->scale = pl->params.scale > 0.0f ? pl->params.scale : 1.0f / sqrtf((float)s.head_dim);
+  constexpr float kLog2e = 1.44269504088896340736f;
+  a->scale = (pl->params.scale > 0.0f ? pl->params.scale : 1.0f / sqrtf((float)s.head_dim)) * kLog2e;
   a->lse = nullptr;
   a->blocks = nullptr;
   a->blocks_out = nullptr;

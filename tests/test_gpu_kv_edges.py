@@ -91,3 +91,38 @@ def test_nan_of_any_payload_stays_nan_in_bf16(nq, n, bits):
     with new_plan(cache, table, q, True) as plan:
         out, lse = run(plan, to_gpu(cache), table, [n], q)
     check(cache, table, [n], q32, True, out, lse)
+
+
+# ------------------------------------------------------------------ the range of queries
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq", [3, 130])
+@pytest.mark.parametrize("exponent", [127, 120, 116, 115, -86, -90, -110])
+def test_queries_at_the_ends_of_the_range(dtype, nq, exponent):
+    """Rows whose largest value is 2^exponent or a little less, at a scale of the scores
+    that brings them to ordinary sizes (for small ones, with large keys)."""
+    rng = np.random.default_rng(nq)
+    cache = filled(rng, 4, 2, 64, k_exponents=(-5, -4) if exponent > 0 else (20, 21))
+    q32 = rng.uniform(-0.99, 0.99, (1, nq, 2, 64)) * 2.0 ** (exponent + (0 if exponent > 126 else 1))
+    q32, q = as_query(q32, dtype)
+    table = np.array([[2, 0, 3, 1]], np.int32)
+    scale = 2.0 ** -min(exponent + 5, 126) if exponent > 0 else 2.0 ** -(exponent + 30)
+    say("[gpu] queries of 2^%d %s %d" % (exponent, dtype, nq))
+    for causal in (True, False):
+        with new_plan(cache, table, q, causal, scale=scale) as plan:
+            out, lse = run(plan, to_gpu(cache), table, [250], q)
+        check(cache, table, [250], q32, causal, out, lse, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq", [3, 130])
+def test_keys_of_zero_at_the_largest_scale_weigh_alike(dtype, nq):
+    """Scores of zero, where the row's power of two times the block's passes fp32."""
+    rng = np.random.default_rng(nq)
+    cache = filled(rng, 4, 1, 64, k_exponents=(44, 44))
+    cache.k[...] = 0
+    q32, q = as_query(rng.uniform(-0.99, 0.99, (1, nq, 1, 64)) * 2.0 ** 127, dtype)
+    table = np.arange(4, dtype=np.int32)[None]
+    say("[gpu] zero keys, queries of 2^127, %s %d" % (dtype, nq))
+    with new_plan(cache, table, q, True, scale=1.0) as plan:
+        out, lse = run(plan, to_gpu(cache), table, [250], q)
+    check(cache, table, [250], q32, True, out, lse, scale=1.0)
