@@ -16,12 +16,20 @@ namespace rc {
 namespace {
 
 constexpr int kRows = 128;               // query rows that are in LDS at a time
-constexpr uint32_t kNone = 0x007FFFFFu;  // key of -infinity: seen by no query
+constexpr uint32_t kNone = 0;            // a block that is not there; any score's key is larger
 
-// Order-preserving map of fp32 to u32.
+// Order-preserving map of fp32 to u32; that of -infinity, the lowest, is 0x007FFFFF.
 __device__ __forceinline__ uint32_t sort_key(float x) {
   const uint32_t u = __float_as_uint(x);
   return u >> 31 ? ~u : u | 0x80000000u;
+}
+
+// x rounded to a whole number, 0 for a NaN (of a NaN in a query, or of an infinity, whose
+// factor is 0): what the instruction gives, and C++'s conversion leaves undefined.
+__device__ __forceinline__ int whole(float x) {
+  int i;
+  asm("v_cvt_i32_f32 %0, %1" : "=v"(i) : "v"(rintf(x)));
+  return i;
 }
 
 // From a lane and the one that CTRL pairs it with (they differ in the bit that `high`
@@ -81,7 +89,7 @@ __global__ __launch_bounds__(64 * WAVES) void kv_select_kernel(KvAttendArgs a) {
   const int q0 = tile * a.q_tile, rows = min(a.q_tile, a.queries - q0) * G;
   const int lim_lo = kv_limit(a, len, q0), lim_hi = kv_limit(a, len, q0 + rows / G - 1);
   const int nb = (lim_hi + 63) / 64;
-  for (int j = tid; j < nb; j += THREADS) keys[j] = 0;
+  for (int j = tid; j < nb; j += THREADS) keys[j] = kNone;
   for (int i = tid; i < 4 * 256; i += THREADS) (&hist[0][0])[i] = 0;
 
   for (int r0 = 0; r0 < rows; r0 += kRows) {
@@ -109,7 +117,7 @@ __global__ __launch_bounds__(64 * WAVES) void kv_select_kernel(KvAttendArgs a) {
       for (int c = 0; c < N; c += 4) {
         uint32_t w = 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) w |= ((uint32_t)(int)rintf(x[c + u] * up) & 255u) << (8 * u);
+        for (int u = 0; u < 4; ++u) w |= ((uint32_t)whole(x[c + u] * up) & 255u) << (8 * u);
         *reinterpret_cast<uint32_t*>(qc + r * QS + c0 + c) = w;
       }
       if (tid % TPR == 0) {
@@ -120,11 +128,13 @@ __global__ __launch_bounds__(64 * WAVES) void kv_select_kernel(KvAttendArgs a) {
     __syncthreads();
     const int cols = min(rows - r0, kRows);
     for (int b64 = wave * 64; b64 < nb; b64 += THREADS) {
-      // two tiles of 32 blocks, all their loads first. A block that does not exist has a
-      // mean of scale NaN, which no maximum takes.
+      // two tiles of 32 blocks, all their loads first. No maximum takes a NaN, so a score that
+      // is one counts as -infinity. A query of the tile sees each block below nb, so one that
+      // exists has a key and can be chosen, whatever its scores; one that does not gets none.
       const int mine = b64 + lane < nb ? kv_block(g, b, b64 + lane) : -1;
       i32x4 mean[2][D / 32];
-      ks[wave][lane] = mine < 0 ? __builtin_nanf("") : g.k_mean_scale[kv_row(g, mine, h)];
+      ks[wave][lane] = mine < 0 ? 0.0f : g.k_mean_scale[kv_row(g, mine, h)];
+      const uint64_t exist = __ballot(mine >= 0);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int block = __shfl(mine, 32 * u + l32);
@@ -162,7 +172,7 @@ __global__ __launch_bounds__(64 * WAVES) void kv_select_kernel(KvAttendArgs a) {
         }
         const float v = max_rows(best, l32);
         const int jj = bt + 8 * (l32 >> 3) + 4 * half + (l32 >> 1 & 3);
-        if ((l32 & 1) == 0 && jj < nb) keys[jj] = max(keys[jj], sort_key(v));
+        if ((l32 & 1) == 0 && jj < nb && (exist >> (jj - b64) & 1)) keys[jj] = max(keys[jj], sort_key(v));
       }
     }
   }

@@ -130,9 +130,11 @@ rc_status_t rc_kv_store(rc_kv_plan_t plan, hipStream_t stream, const rc_kv_cache
  * The score of a block for a tile is the largest over the tile's queries that see
  * its first token and over the query heads of the key head. The keep_blocks blocks
  * of the highest score are chosen, ties to the lower index; with RC_KV_CAUSAL the
- * blocks of the tile's own positions come first. blocks: device int32
- * [batch][kv_heads][ceil(queries / q_tile)][keep_blocks], ascending, -1 after the
- * last.
+ * blocks of the tile's own positions come first. Every block that is there and that a
+ * query of the tile sees can be chosen: a score that is NaN (a query that holds an
+ * infinity has no other) counts as -infinity, and that is the lowest score. A NaN in a
+ * query counts as 0 here. blocks: device int32 [batch][kv_heads][ceil(queries / q_tile)]
+ * [keep_blocks], ascending, -1 after the last.
  * max_len: a bound of kv_len that the host knows (0: 64 * seq_blocks). Longer
  * lengths are cut to it, and to 64 * seq_blocks; negative ones count as 0. */
 rc_status_t rc_kv_select(rc_kv_plan_t plan, hipStream_t stream, const rc_kv_cache_t* cache,

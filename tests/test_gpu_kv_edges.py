@@ -126,3 +126,44 @@ def test_keys_of_zero_at_the_largest_scale_weigh_alike(dtype, nq):
     with new_plan(cache, table, q, True, scale=1.0) as plan:
         out, lse = run(plan, to_gpu(cache), table, [250], q)
     check(cache, table, [250], q32, True, out, lse, scale=1.0)
+
+
+# ------------------------------------------------------------------ choice of blocks
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim,kh", [(64, 1), (128, 2)])
+@pytest.mark.parametrize("nq,q_tile,keep,causal", [(1, 1, 3, True), (3, 1, 3, False), (5, 1, 1, True), (3, 1, 40, True),
+                                                   (130, 128, 4, True), (130, 128, 4, False), (7, 128, 64, False)])
+@pytest.mark.parametrize("what", ["infinite query", "nan query", "scores past fp32", "mean of scale nan"])
+def test_select_scores_that_are_not_finite(dtype, dim, kh, nq, q_tile, keep, causal, what):
+    """A block that is there and seen can be chosen whatever its score, and the tile's own
+    come first: a query that holds an infinity reaches attention, and its output is NaN."""
+    rng = np.random.default_rng(nq + dim + keep)
+    lens, nb = [640, 333], 10
+    cache = filled(rng, 2 * nb, kh, dim)
+    table = rng.permutation(2 * nb).reshape(2, nb).astype(np.int32)
+    table[0, 4] = -1
+    q32, _ = values(rng, (2, nq, 2 * kh, dim), dtype)
+    if what == "infinite query":
+        q32[:, nq // 2, :, 3] = np.inf
+        q32[:, 0, 0, 9] = -np.inf
+    elif what == "nan query":
+        q32[:, nq // 2, :, 3] = np.nan
+        q32[:, 0, 0] = np.nan
+    elif what == "scores past fp32":
+        q32[:, ::2] *= np.float32(2.0 ** 115)
+        cache.k_mean_scale[...] *= np.float32(2.0 ** 5)
+    else:
+        cache.k_mean_scale[table[0, 1]] = np.nan
+        cache.k_mean_scale[table[1, 5]] = np.nan
+    kv = to_gpu(cache)
+    q32, q = as_query(q32, dtype)
+    want = np.stack([kv_dense.choose(cache, table[b], lens[b], q32[b], causal, q_tile, keep) for b in range(2)])
+    blocks = torch.full(want.shape, 12345, dtype=torch.int32, device=DEV)
+    say("[gpu] select %s %s %d/%d queries %d tile %d keep %d causal %d" % (what, dtype, dim, kh, nq, q_tile, keep, causal))
+    with new_plan(cache, table, q, causal, q_tile=q_tile, keep_blocks=keep) as plan:
+        plan.select(kv, ints(lens), q, blocks, table=ints(table))
+        torch.cuda.synchronize()
+        assert np.array_equal(blocks.cpu().numpy(), want)
+        out, lse = run(plan, kv, table, lens, q, blocks=blocks)
+    if what != "scores past fp32":                              # there the scores of attention are as large
+        check(cache, table, lens, q32, causal, out, lse, want, q_tile)
