@@ -112,7 +112,8 @@ __global__ __launch_bounds__(64 * WAVES) void kv_select_kernel(KvAttendArgs a) {
         }
       }
       top = group_max<TPR>(top);
-      const float up = top > 0.0f ? 127.0f * (1.0f / top) : 0.0f;
+      float up = 127.0f * (1.0f / top);
+      if (!(up < INFINITY)) up = 0.0f;  // a row of zeros, or of less than 2^-121
 #pragma unroll
       for (int c = 0; c < N; c += 4) {
         uint32_t w = 0;

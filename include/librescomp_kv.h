@@ -125,7 +125,8 @@ rc_status_t rc_kv_store(rc_kv_plan_t plan, hipStream_t stream, const rc_kv_cache
  * kv_len[b] tokens. q: [batch][queries][q_heads][head_dim] in the plan's dtype.
  *   score(query, head, block) = (float(qc . k_mean) * k_mean_scale) * max|q|, where
  *   qc = q * ((1 / max|q|) * 127), rounded to nearest even, in 8 bits (each
- *   operation rounded to fp32; the products of qc and k_mean are whole numbers and
+ *   operation rounded to fp32; where the factor is not finite, for rows of zeros and of
+ *   less than 2^-121, qc is 0; the products of qc and k_mean are whole numbers and
  *   their sum is exact, so the choice does not depend on the order of a sum).
  * The score of a block for a tile is the largest over the tile's queries that see
  * its first token and over the query heads of the key head. The keep_blocks blocks

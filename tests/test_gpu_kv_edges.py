@@ -167,3 +167,24 @@ def test_select_scores_that_are_not_finite(dtype, dim, kh, nq, q_tile, keep, cau
         out, lse = run(plan, kv, table, lens, q, blocks=blocks)
     if what != "scores past fp32":                              # there the scores of attention are as large
         check(cache, table, lens, q32, causal, out, lse, want, q_tile)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_select_rows_near_the_smallest_numbers(dtype):
+    """Rows whose factor 127 / max|q| passes fp32 score 0: ties, the lowest blocks."""
+    rng = np.random.default_rng(12)
+    cache = filled(rng, 8, 1, 64)
+    kv = to_gpu(cache)
+    table = np.arange(8, dtype=np.int32)[None]
+    q32, _ = values(rng, (1, 4, 1, 64), dtype)
+    for i, size in enumerate((2.0 ** -120, 2.0 ** -124, 1e-38, 2e-40)):
+        q32[0, i] *= np.float32(size) / np.abs(q32[0, i]).max()
+    q32, q = as_query(q32, dtype)
+    want = kv_dense.choose(cache, table[0], 512, q32[0], False, 1, 3)
+    assert np.array_equal(want[0, 1:], np.tile([0, 1, 2], (3, 1)))
+    blocks = torch.empty((1,) + want.shape, dtype=torch.int32, device=DEV)
+    say("[gpu] select of tiny rows %s" % dtype)
+    with new_plan(cache, table, q, False, q_tile=1, keep_blocks=3) as plan:
+        plan.select(kv, ints([512]), q, blocks)
+        torch.cuda.synchronize()
+    assert np.array_equal(blocks.cpu().numpy()[0], want)
