@@ -90,15 +90,24 @@ __device__ __forceinline__ void to_half(const float (&p)[8], half8_t& hi, half8_
   }
 }
 
-// Entries of a list of blocks before the first one that is negative or not below
-// `reach`. Called by whole waves.
-__device__ __forceinline__ int list_length(const int32_t* list, int keep, int reach, int lane) {
+// Blocks that the queries of a tile see.
+__device__ __forceinline__ int tile_reach(const KvAttendArgs& a, int len, int tile) {
+  return (kv_limit(a, len, min((tile + 1) * a.q_tile, a.queries) - 1) + 63) / 64;
+}
+
+// A list of blocks ends at its first entry that is negative or not below `end`, the blocks
+// that its tile sees; of the entries before, those up to the last one below `reach`, the
+// blocks that these rows see. Called by whole waves.
+__device__ __forceinline__ int list_length(const int32_t* list, int keep, int end, int reach, int lane) {
+  int n = 0;
   for (int i = 0; i < keep; i += 64) {
     const int j = i + lane < keep ? list[i + lane] : -1;
-    const uint64_t end = __ballot(j < 0 || j >= reach);
-    if (end) return i + __builtin_ctzll(end);
+    const uint64_t stop = __ballot(j < 0 || j >= end);
+    const uint64_t seen = __ballot(j < reach) & (stop ? (stop & -stop) - 1 : ~(uint64_t)0);
+    if (seen) n = i + 64 - __builtin_clzll(seen);
+    if (stop) break;
   }
-  return keep;
+  return n;
 }
 
 // Takes in probability e of 16 (in order): the sum, and when it closes a pair, f16
@@ -160,18 +169,18 @@ __device__ __forceinline__ float2 get_pair(const float* p) {
 // The blocks that a wave reads, entries from, from + step, ... below to, one after the
 // other, without a load in the way: the wave's 64 lanes hold the next 64 (index, pool
 // block, scales), loaded at once, and hand them out one by one. Blocks that do not
-// exist are skipped.
+// exist are skipped, and those of a list that these rows do not see (from `reach` on).
 struct Walk {
   const KvGeom& g;
   const int32_t* list;
-  int b, h, base, to, step, lane;
+  int b, h, base, to, step, reach, lane;
   uint64_t left;  // entries of these 64 still to come
   int lane_block;
   uint32_t lane_what;  // index (16 bits), exponents + 64 of K's and V's scales (8 bits each)
 
   __device__ __forceinline__ Walk(const KvGeom& g, const int32_t* list, int b, int h, int from, int to, int step,
-                                  int lane)
-      : g(g), list(list), b(b), h(h), base(from - 64 * step), to(to), step(step), lane(lane), left(0) {}
+                                  int reach, int lane)
+      : g(g), list(list), b(b), h(h), base(from - 64 * step), to(to), step(step), reach(reach), lane(lane), left(0) {}
   __device__ __forceinline__ void fill() {
     base += 64 * step;
     lane_block = -1;
@@ -179,7 +188,7 @@ struct Walk {
     if (at < to) {
       const int j = list ? list[at] : at;
       lane_what = (uint32_t)j;
-      lane_block = kv_block(g, b, j);
+      if (j < reach) lane_block = kv_block(g, b, j);
     }
     if (lane_block >= 0) {
       const int64_t row = kv_row(g, lane_block, h);
@@ -245,7 +254,7 @@ __global__ __launch_bounds__(256, F32 ? 2 : 3) void kv_attend_few_kernel(KvAtten
   if (a.blocks) {
     const int tile = (r0 / g.group) / a.q_tile;
     list = a.blocks + (((int64_t)b * g.kv_heads + h) * a.tiles + tile) * a.keep;
-    count = list_length(list, a.keep, reach, lane);
+    count = list_length(list, a.keep, tile_reach(a, len, tile), reach, lane);
   }
   int parts, from, to;
   if (!part_of(a, count, split, parts, from, to)) return;
@@ -282,7 +291,7 @@ __global__ __launch_bounds__(256, F32 ? 2 : 3) void kv_attend_few_kernel(KvAtten
   for (int d = 0; d < ND; ++d) o[d] = f32x4{0, 0, 0, 0};
   float m_run = kLowest, l_run = 0.0f;
   int ev_cur = 0;
-  Walk walk(g, list, b, h, from + wave, to, 4, lane);
+  Walk walk(g, list, b, h, from + wave, to, 4, reach, lane);
   int block, slot;
   for (int j; (j = walk.next(block, slot)) >= 0;) {
     const int64_t row = kv_row(g, block, h);
@@ -525,7 +534,7 @@ __global__ __launch_bounds__(256, D == 128 && !F32 ? 2 : 3) void kv_attend_many_
   int count = reach;
   if (a.blocks) {
     list = a.blocks + (((int64_t)b * g.kv_heads + h) * a.tiles + (r0 / g.group) / a.q_tile) * a.keep;
-    count = list_length(list, a.keep, reach, lane);
+    count = list_length(list, a.keep, tile_reach(a, len, (r0 / g.group) / a.q_tile), reach, lane);
   }
   int parts, from, to;
   if (!part_of(a, count, split, parts, from, to)) return;
@@ -592,7 +601,7 @@ __global__ __launch_bounds__(256, D == 128 && !F32 ? 2 : 3) void kv_attend_many_
     for (int d = 0; d < ND; ++d) vr[d] = *reinterpret_cast<const u32x4*>(v + (v_at + (uint32_t)d * (32 * 16)));
   };
 
-  Walk walk(g, list, b, h, from + wave, to, 4, lane);
+  Walk walk(g, list, b, h, from + wave, to, 4, reach, lane);
   int block, slot, j = walk.next(block, slot);
   if (j >= 0) load_k(block, 0);
   while (j >= 0) {

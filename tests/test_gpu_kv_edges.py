@@ -188,3 +188,26 @@ def test_select_rows_near_the_smallest_numbers(dtype):
         plan.select(kv, ints([512]), q, blocks)
         torch.cuda.synchronize()
     assert np.array_equal(blocks.cpu().numpy()[0], want)
+
+
+# ------------------------------------------------------------------ lists
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("qh,nq,n", [(1, 60, 300), (1, 128, 640), (2, 128, 640), (4, 16, 300)])
+@pytest.mark.parametrize("entries", [[-1, 0], [-1, -2, 0], [-2, -1, -3], [1, 1, 0], [0, -1, 0, -1], [-1, 0, 99, 1], [-1]])
+def test_lists_in_any_order(dtype, qh, nq, n, entries):
+    """A tile's list, counted from the last block that the tile sees where negative, in the
+    order given, with entries that repeat: rows that do not see a block yet go on after it."""
+    rng = np.random.default_rng(nq + n)
+    nb = 11
+    cache = filled(rng, nb, 1, 64)
+    table = rng.permutation(nb).reshape(1, nb).astype(np.int32)
+    q32, q = values(rng, (1, nq, qh, 64), dtype)
+    last = -(-n // 64)
+    lst = [last + j if j < 0 else j for j in entries]
+    keep = 5
+    lists = np.full((1, 1, 1, keep), -1, np.int32)
+    lists[0, 0, 0, :len(lst)] = lst
+    say("[gpu] list %s %s %d queries of %d heads" % (lst, dtype, nq, qh))
+    with new_plan(cache, table, q, True, q_tile=128, keep_blocks=keep) as plan:
+        out, lse = run(plan, to_gpu(cache), table, [n], q, blocks=ints(lists))
+    check(cache, table, [n], q32, True, out, lse, lists, 128)
