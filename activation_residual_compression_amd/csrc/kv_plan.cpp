@@ -152,7 +152,9 @@ rc_status_t check_cache(const rc_kv_cache_t* c) {
   return RC_OK;
 }
 
-// A view of [batch][tokens][heads][dim]; strides of dimensions of size 1 do not count.
+// A view of [batch][tokens][heads][dim]; strides of dimensions of size 1 do not count. The
+// rows of an output must not overlap: in order of their strides, each dimension's passes
+// what those before it span.
 rc_status_t rows_of(const rc_kv_view_t* v, int64_t batch, int64_t tokens, int64_t heads, int64_t dim, bool out,
                     rc::KvRows* r) {
   if (!v || (!v->data && tokens > 0)) return RC_ERR_INVALID_ARG;
@@ -164,6 +166,16 @@ rc_status_t rows_of(const rc_kv_view_t* v, int64_t batch, int64_t tokens, int64_
     if (n[i] <= 1) st[i] = 0;
     else if (st[i] < (out ? dim : 0) || st[i] >= (int64_t)1 << 40) return RC_ERR_INVALID_ARG;
     if (st[i] % unit) return RC_ERR_ALIGNMENT;
+  }
+  if (out) {
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int x, int y) { return st[x] < st[y]; });
+    __int128 span = dim;
+    for (int i : order) {
+      if (n[i] <= 1) continue;
+      if (st[i] < span) return RC_ERR_INVALID_ARG;
+      span += (__int128)st[i] * (n[i] - 1);
+    }
   }
   *r = {v->data, st[0], st[1], st[2]};
   return RC_OK;

@@ -78,8 +78,10 @@ typedef struct {
 /* Rows of head_dim contiguous values: element (b, t, h, d) of a tensor
  * [batch][tokens][heads][head_dim] is data[b * batch_stride + t * token_stride +
  * h * head_stride + d]. Strides are in elements, not negative, and keep every row
- * 16-byte aligned; an input's strides may be 0. A call with no tokens or queries
- * reads and writes nothing (data may be NULL) and returns RC_OK. */
+ * 16-byte aligned; an input's strides may be 0. An output's dimensions (those of more
+ * than one) nest: in order of their strides, each stride passes what the dimensions
+ * before it span, so no two rows overlap; any view of whole rows of a tensor does. A call
+ * with no tokens or queries reads and writes nothing (data may be NULL) and returns RC_OK. */
 typedef struct {
   void* data;
   rc_dtype_t dtype;
