@@ -211,3 +211,117 @@ def test_lists_in_any_order(dtype, qh, nq, n, entries):
     with new_plan(cache, table, q, True, q_tile=128, keep_blocks=keep) as plan:
         out, lse = run(plan, to_gpu(cache), table, [n], q, blocks=ints(lists))
     check(cache, table, [n], q32, True, out, lse, lists, 128)
+
+
+# ------------------------------------------------------------------ keys split over blocks of threads
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("qh,kh", [(4, 2), (3, 3), (20, 1)])
+def test_one_plan_many_calls_in_several_parts(dtype, dim, qh, kh):
+    """Several sequences of very different lengths, heads and groups, one plan for calls of
+    changing numbers of queries and bounds of the lengths: each against 64 bits."""
+    rng = np.random.default_rng(dim + qh)
+    nb, lens = 40, [64 * 40, 0, 1, 700, 64 * 39 + 5]
+    B = len(lens)
+    cache = filled(rng, 2 * nb, kh, dim)
+    table = rng.integers(0, 2 * nb, (B, nb)).astype(np.int32)      # sequences may share what they read
+    table[3, 2], table[4, 20] = -1, 2 * nb
+    kv = to_gpu(cache)
+    for causal in (True, False):
+        q32, q = values(rng, (B, 150, qh, dim), dtype)
+        with new_plan(cache, table, q, causal) as plan:
+            assert plan.workspace_bytes > 0                       # it has several parts at these sizes
+            for nq, max_len in ((1, 0), (1, 0), (150, 0), (2, 0), (150, 1000), (1, 1500), (70, 0), (1, 100), (150, 0), (1, 0)):
+                say("[gpu] parts %s %d heads %d/%d queries %d max %d causal %d" % (dtype, dim, qh, kh, nq, max_len, causal))
+                i = int(rng.integers(0, 151 - nq))
+                out, lse = run(plan, kv, table, lens, q[:, i:i + nq], max_len=max_len)
+                check(cache, table, lens, q32[:, i:i + nq], causal, out, lse, max_len=max_len)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("ascending", [True, False])
+@pytest.mark.parametrize("nq,q_tile", [(1, 1), (3, 1), (128, 128), (200, 128)])
+def test_long_lists_in_several_parts(dtype, nq, q_tile, ascending):
+    """Lists of more than 64 entries, some missing, for ragged sequences; twice on one plan."""
+    rng = np.random.default_rng(nq)
+    nb, keep, lens = 130, 100, [64 * 130, 64 * 70 + 3, 0]
+    cache = filled(rng, 140, 2, 64)
+    table = np.stack([rng.permutation(140)[:nb] for _ in lens]).astype(np.int32)
+    table[0, 3] = -1
+    q32, q = values(rng, (3, nq, 4, 64), dtype)
+    tiles = -(-nq // q_tile)
+    lists = np.full((3, 2, tiles, keep), -1, np.int32)
+    for b, n in enumerate(lens):
+        for h in range(2):
+            for t in range(tiles):
+                some = rng.permutation(max(1, -(-n // 64)))[:keep - 7 * t]
+                some = np.sort(some) if ascending else some
+                lists[b, h, t, :len(some)] = some
+    kv = to_gpu(cache)
+    with new_plan(cache, table, q, True, q_tile=q_tile, keep_blocks=keep) as plan:
+        for again in range(2):
+            say("[gpu] long lists %s queries %d call %d" % (dtype, nq, again))
+            out, lse = run(plan, kv, table, lens, q, blocks=ints(lists))
+            check(cache, table, lens, q32, True, out, lse, lists, q_tile)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,nq", [(768, 1), (512, 65)])
+def test_more_than_256_blocks_in_one_part(dtype, B, nq):
+    """A wave walks more than 64 blocks: so many sequences that none is split. All but the
+    last two are the same one, and equal to the bit."""
+    rng = np.random.default_rng(B)
+    nb, n = 300, 64 * 300 - 9
+    cache = filled(rng, nb, 1, 64)
+    table = np.tile(rng.permutation(nb).astype(np.int32), (B, 1))
+    table[B - 2] = rng.permutation(nb)
+    table[B - 1, 4:280] = -1
+    lens = [n] * (B - 1) + [64 * 290]
+    q32, q = values(rng, (1, nq, 1, 64), dtype)
+    q, q32 = q.expand(B, nq, 1, 64), np.broadcast_to(q32, (B, nq, 1, 64))
+    say("[gpu] %d sequences of %d blocks, %d queries, %s" % (B, nb, nq, dtype))
+    with new_plan(cache, table, q, False) as plan:
+        out, lse = run(plan, to_gpu(cache), table, lens, q)
+    assert all(torch.equal(x[1:B - 2], x[:1].expand_as(x[1:B - 2])) for x in (out, lse))
+    check(cache, table, lens, q32, False, out, lse, which=(0, B - 2, B - 1))
+
+
+@pytest.mark.parametrize("nq,q_tile", [(1, 0), (1, 1), (70, 0)])
+def test_graph_replays_of_calls_in_several_parts(nq, q_tile):
+    """A captured call whose keys are split, replayed while the lengths move, with the
+    plan's own eager calls between the replays."""
+    rng = np.random.default_rng(nq + q_tile)
+    nb, kh, qh, d = 40, 2, 4, 64
+    cache = filled(rng, 2 * nb, kh, d)
+    table = rng.permutation(2 * nb).reshape(2, nb).astype(np.int32)
+    kv = to_gpu(cache)
+    q32, q = values(rng, (2, nq, qh, d), "bf16")
+    kw = dict(q_tile=1, keep_blocks=30) if q_tile else {}
+    lens, tab = ints([64 * nb, 900]), ints(table)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device=DEV)
+    blocks = torch.empty(2, kh, nq, 30, dtype=torch.int32, device=DEV) if q_tile else None
+    with new_plan(cache, table, q, True, **kw) as plan:
+        def step():
+            if q_tile:
+                plan.select(kv, lens, q, blocks, table=tab)
+            plan.attend(kv, lens, q, out, lse, table=tab, blocks=blocks)
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for i in range(5):
+            now = [64 * nb - 7 * i, 900 + 130 * i if i % 2 else 3]
+            lens.copy_(ints(now))
+            torch.cuda.synchronize()
+            out.fill_(77.0)
+            lse.fill_(77.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            say("[gpu] replay %d of %d queries, lists %d" % (i, nq, q_tile))
+            lists = blocks.cpu().numpy() if q_tile else None
+            check(cache, table, now, q32, True, out, lse, lists, q_tile)
+            kept = out.clone(), lse.clone()
+            step()
+            torch.cuda.synchronize()
+            assert torch.equal(out, kept[0]) and torch.equal(lse, kept[1])
