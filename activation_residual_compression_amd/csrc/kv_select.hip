@@ -254,12 +254,18 @@ __global__ __launch_bounds__(64 * WAVES) void kv_select_kernel(KvAttendArgs a) {
   for (int i = over + min(ties, (int)want) + tid; i < a.keep; i += THREADS) out[i] = -1;
 }
 
-// 8 waves score the blocks of a tile where the tiles are too few to fill the CUs.
+// 8 waves score the blocks of a tile where the CUs hold all tiles at once that way (one each
+// at 128 channels, two at 64, whose registers fit twice) and 4 waves would take more than
+// one turn (64 blocks a wave). Measured in us, 4 and 8 waves, single tokens of 8 key heads:
+// 128 channels, 256 tiles of 313 blocks 10.9 and 9.0, of 625 14.1 and 11.2; 288 tiles 12.2
+// and 15.8, 16.7 and 20.2; 512 12.3 and 16.2, 19.5 and 25.1. 64 channels, 512 tiles of 625
+// blocks 17.8 and 16.7, 576 19.3 and 23.8. With 64 blocks or 256, where the rule takes 4:
+// 256 tiles 8.0 and 7.3, 8.8 and 8.2 at 128 channels, 512 tiles 7.3 and 8.3, 8.4 and 9.1 at 64.
 template <int D, typename IN>
 hipError_t run(const KvAttendArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.tiles, (unsigned)a.g.kv_heads, (unsigned)a.g.batch);
   const int blocks = (a.max_len + 63) / 64;
-  if ((int64_t)a.tiles * a.g.kv_heads * a.g.batch <= 512 && blocks > 256)
+  if ((int64_t)a.tiles * a.g.kv_heads * a.g.batch <= (D == 64 ? 512 : 256) && blocks > 256)
     kv_select_kernel<D, IN, 8><<<grid, 512, (size_t)blocks * 4, s>>>(a);
   else
     kv_select_kernel<D, IN, 4><<<grid, 256, (size_t)blocks * 4, s>>>(a);
