@@ -5,8 +5,12 @@
 // results. A query row is scaled by a power of two so that its largest value lies
 // in [2^14, 2^15): a bf16 query is then exact in f16 (values under 2^-29 of the
 // row's largest lose bits), and an fp32 query is the sum of two f16 (22 bits).
-// Probabilities are rounded to f16 (11 bits; bf16 outputs keep 8), or are the sum
-// of two f16 for fp32. Scores, statistics and outputs are accumulated in fp32.
+// Probabilities are rounded to f16 (11 bits) before they meet V where the outputs are
+// bf16 (8 bits), or are the sum of two f16 for fp32; the sum of a row takes them as they
+// were. Scores, statistics and outputs are accumulated in fp32. Two f16 for bf16 outputs
+// too was measured: image share 138 -> 193 us, video share 701 -> 1002, prompts 94 -> 126,
+// for an error against 64 bits of 1.659e-3 instead of 1.671e-3 (relative, of the whole
+// output; the rounding to bf16 alone is 1.659e-3): not taken.
 //
 // Softmax in base 2: with c = scale * log2(e) * (scale of the row and block),
 // p = 2^(S c - m + kBias), m the running maximum of S c (in the kernel for many rows
@@ -223,10 +227,11 @@ struct Walk {
 // bound: every code is read once for 16 rows. Three waves a SIMD without a prefetch
 // beat two with the next block's loads in flight on long sequences (716 us against
 // 739 for 64 of 32768 tokens). Measured with one query of four heads to a key head, 8
-// key heads of 128: 64 sequences of 32768 tokens 710 us (6.05 TB/s), 4 of 65536 95 us
-// (5.7), 32 ragged ones of up to 8192 68 us (4.5: the longest is the last to end); one
-// token over 333, 24 heads: 7.2 us, most of it the chain of dependent reads (length,
-// table, codes) and the launch.
+// key heads of 128: 64 sequences of 32768 tokens 710 us (6.05 TB/s), 4 of 65536 97 us
+// (5.5), 32 ragged ones of up to 8192 61 us (5.0, in one part: a block of threads on each CU,
+// which holds three, and most end before the longest), in fp32 91. One token over 333, 24
+// heads: 7.2 us, most of it the launch and the chain of reads that wait for one another:
+// length, queries, table, scales, codes (with lists two more).
 template <int D, bool F32>
 __global__ __launch_bounds__(256, F32 ? 2 : 3) void kv_attend_few_kernel(KvAttendArgs a) {
   constexpr int ND = D / 16, NQ = D / 64;
@@ -465,7 +470,9 @@ __global__ __launch_bounds__(256, F32 ? 2 : 3) void kv_attend_few_kernel(KvAtten
 // 64: 695 us, 732 in plain order; over 70 chosen blocks each 220 and 228). Otherwise tiles
 // are in order of length, the longest first, over all heads: runs would leave XCDs with
 // the long sequences' tiles alone (three ragged causal sequences: 195 us in runs, 115 so),
-// and one head to one XCD gained nothing (two of 24 heads of 128: 139 us either way).
+// and one head to one XCD gained nothing (two of 24 heads of 128: 139 us either way). Where
+// heads times sequences and 8 share a factor this order too keeps a sequence to some XCDs
+// (two sequences of four heads: each to four of them).
 struct Place {
   int b, h, split, tile;
 };
@@ -506,9 +513,9 @@ __device__ __forceinline__ float max_halves(float x) {
 // block): video share 764 -> 695 us, its block-selected form 250 -> 220, ragged causal
 // prompts 110 -> 95, image share 139 -> 139, in fp32 135 -> 141; there LDS writes cost
 // as much as the conversions. Bound by the vector units next to the matrix units: of
-// their cycles 63 % and 51 % at 128 channels, 87 % and 47 % at 64 (exponentials, sums and
+// their cycles 63 % and 51 % at 128 channels, 88 % and 47 % at 64 (exponentials, sums and
 // the conversions of K and V, of which 64 rows share one). Measured: 1152 queries over
-// 4608 tokens, 2 x 24 heads of 128, 139 to 144 us on different cards (up to 940 TFLOP/s);
+// 4608 tokens, 2 x 24 heads of 128, 138 to 144 us on different cards (up to 940 TFLOP/s);
 // 4444 over 17776, 30 heads of 64, 695 to 723 us (up to 870).
 template <int D, bool F32>
 __global__ __launch_bounds__(256, D == 128 && !F32 ? 2 : 3) void kv_attend_many_kernel(KvAttendArgs a) {
@@ -804,7 +811,7 @@ __global__ __launch_bounds__(256, D == 128 && !F32 ? 2 : 3) void kv_attend_many_
 
 // ------------------------------------------------------------------ joining splits
 // D / 4 lanes a row: out = sum O_s 2^(m_s - m) / sum l_s 2^(m_s - m), parts in order. HBM
-// (or last-level cache) bound: 133 thousand rows of 64 in two parts, 20 us.
+// (or last-level cache) bound: 133 thousand rows of 64 in two parts, 21 us.
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void kv_attend_join_kernel(KvAttendArgs a) {
   typedef typename std::conditional<F32, float, uint16_t>::type IO;

@@ -72,14 +72,28 @@ Way way_of(const rc_kv_plan* pl, int64_t queries, int64_t blocks, bool chosen, i
       }
     }
   } else {
-    // Blocks of threads that the CUs hold at once, and rows of each (the kernel's).
+    // Blocks of threads that the CUs run at full rate, two each, and rows of each (the
+    // kernel's). Three of the four forms fit a third, but then each takes longer a step:
+    // planned with 768 the video share takes 713 us and not 698, fp32 image share 151 and
+    // 141, 1111 queries over 8888 in fp32, 30 heads of 64, 210 and 182; a few calls gain
+    // (3000 over 3000, 16 heads of 64 on 2, 48 and 64).
     const int64_t at_once = 512, tile = s.head_dim == 128 && pl->dtype == RC_F32 ? 32 : 64;
     const int64_t base = heads * ceil_div(rows, tile);
-    // The time in steps of four blocks, one a wave (about 3.6 us where the CUs are
-    // full), and 3 for the start and end of a block of threads: whole rounds of equal
+    // The time in steps of four blocks, one a wave (about 3.6 us where the CUs are full),
+    // and one more for the start and end of a block of threads: whole rounds of equal
     // parts, or for causal rows, whose parts differ and are started longest first, the
     // average and half the longest. Partial results cost a write and a read, and the
-    // launch that joins them.
+    // launch that joins them 1.5 steps. Measured in us, as it is and with one weight
+    // changed, over 30 calls, those that differ by more than 2 % most:
+    //   start and end 1   at 0: video share 699 and 718, fp32 2222 over 8000, 16 / 4 heads of
+    //                     128, 290 and 304, 500 over 5000, 24 heads, 80 and 77; at 3: causal
+    //                     512 over 8000, 24 heads of 128, 66 and 76, 3000 over 3000 64 and 48
+    //   longest part 0.5  at 0: causal 512 over 8000 66 and 76, 1000 over 1000, 12 heads of
+    //                     64, 17.0 and 13.5; at 1: causal 2000 over 4000, 2 x 12 heads of 64,
+    //                     55 and 64, fp32 4444 over 8888 472 and 488
+    //   write and read    at 0: video share 699 and 720, chosen blocks of it 194 and 213,
+    //                     causal 4000 over 4000, 16 / 4 heads of 128, 77 and 112
+    //   launch 1.5        at 0: none; at 4: 3000 over 3000 64 and 48, 1000 over 1000 17.0 and 13.4
     const bool causal = (pl->params.flags & RC_KV_CAUSAL) && !chosen;
     double best = 0.0;
     for (int64_t p = 1; p <= std::min({(int64_t)16, ceil_div(blocks, 8), std::max<int64_t>(most_rows / (heads * rows), 1)});

@@ -6,10 +6,12 @@
 // largest value) are part of its definition. One block of threads scores all
 // blocks for one tile of queries of one key head (v_mfma_i32_32x32x32_i8, mean
 // keys as rows, queries as columns), then picks the k best by a radix select on
-// the scores' bits in LDS. Bound by latency: the chain of reads (length, table, means)
-// and four digits of the select. Measured: 32 of up to 1024 blocks for 8 sequences and
-// 8 key heads 13.7 us; 70 of 278 for 35 tiles of 30 heads 29.5 us; 24 of 125 for 16
-// tiles of 4 x 128 fp32 rows, 4 heads, 2 sequences 34 us.
+// the scores' bits in LDS. Bound by latency and by waves without work: the chain of reads
+// (length, queries, table, means), in bf16 a thread's query loads, each of which waits for
+// the one before, and four digits of the select; waves take 64 blocks at a time, so 125
+// blocks leave two of four without any. Measured: 32 of up to 1024 blocks for 8 sequences
+// and 8 key heads 13.6 us (either type); 70 of 278 for 35 tiles of 30 heads 30 us (vector
+// units 80 % busy); 24 of 125 for 16 tiles of 4 x 128 fp32 rows, 4 heads, 2 sequences 34 us.
 #include "kv_device.hpp"
 
 namespace rc {

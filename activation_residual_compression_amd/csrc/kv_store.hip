@@ -3,10 +3,11 @@
 // One block of threads owns one 64-token block of one key head, of K or of V:
 // every scale is the maximum over exactly what one thread block holds, so a
 // single pass over the new values is enough (read once, 2 or 4 B an element; one
-// byte written). HBM bound for whole sequences: 4 x 4608 tokens of 24 x 128 bf16 68 to
-// 72 us (5.0 to 4.7 TB/s), 4444 of 30 x 64 fp32 15.8 us (5.4). For single tokens the
-// launch and the chain of reads (start, table, codes) are what it costs: 16 sequences,
-// 8 heads of 128, 5.9 us.
+// byte written). HBM bound for whole sequences (in bf16 each of a thread's loads waits
+// for the one before): 4 x 4608 tokens of 24 x 128 bf16 68 to 72 us (5.0 to 4.7 TB/s), 4444
+// of 30 x 64 fp32 16 us (5.3). For single tokens the launch and the chain of reads that
+// wait for one another (start, table, new values, scale and, of V, earlier codes) are
+// what it costs: 16 sequences, 8 heads of 128, 6.1 us, in fp32 6.4.
 #include "kv_device.hpp"
 
 namespace rc {

@@ -568,7 +568,8 @@ class KvPlan:
 
     def attend(self, cache, kv_len, q, out, lse=None, table=None, max_len=0, blocks=None, stream=None):
         """Attention of q over the cache (over the chosen blocks, if given); writes out,
-        like q, and lse, fp32 [batch, queries, q_heads]."""
+        like q, and lse, fp32 [batch, queries, q_heads]. In bf16 the softmax weights have 11
+        bits in their product with the values, in fp32 queries and weights have 22."""
         queries = q.shape[1]
         view = self._rows(q, self.q_heads, "q", None, self.dtype)
         to = self._rows(out, self.q_heads, "out", queries, self.dtype)

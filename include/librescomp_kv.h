@@ -153,6 +153,11 @@ rc_status_t rc_kv_select(rc_kv_plan_t plan, hipStream_t stream, const rc_kv_cach
  * lse (NULL, or fp32 [batch][queries][q_heads]): the natural logarithm of the sum
  * of the exponentials, to join this result with attention over other tokens. A
  * query that sees no token, or whose scores are all -infinity, gets 0 and -infinity.
+ * Precision: sums, the running maximum and outputs are held in fp32 and rounded once.
+ * With bf16 outputs the weights are rounded to f16 (11 bits) for their product with v, not
+ * for their sum: before the rounding to bf16 an output is within about 2^-11 of the
+ * weighted mean of |v|. In fp32, queries and weights are sums of two f16 (22 bits). Values
+ * of a query under 2^-29 of its largest lose bits.
  * NaN: a key's makes the outputs and the lse of the queries that see it NaN; a query's,
  * or scores of +infinity, its own. A value's reaches the outputs, not the lse, of the
  * queries that see it and, with RC_KV_CAUSAL, may reach the outputs of earlier queries of
