@@ -56,9 +56,9 @@ Way way_of(const rc_kv_plan* pl, int64_t queries, int64_t blocks, bool chosen, i
     // The time in microseconds: the bytes at 5.8 TB/s, or the waves' blocks one after
     // the other (2.4 each) where that is longer; 4 for the start and end of a round of
     // the blocks of threads that the CUs hold at once; for the join 5, and 0.4 for each
-    // part. Measured: 32 sequences of 8192 tokens, 8 key heads of 128, 95 us in one part
-    // and 103, 102, 108, 111 in 2, 3, 4, 6; 4 of 65536 tokens 108 us in 7 parts, 110 in
-    // 24, 118 in 32; 8 of 32 chosen blocks 12.0 us in 4, 13.7 in 8, 13.1 in 2.
+    // part. Measured: 32 sequences of 8192 tokens, 8 key heads of 128, 94 us in one part
+    // and 98, 101, 107, 109 in 2, 3, 4, 6; 4 of 65536 tokens 97 us in 7 parts, 113 in 4, 109
+    // in 24, 118 in 32; 8 of 32 chosen blocks 11.3 us in 4, 12.5 in 2, 12.9 in 8.
     const int64_t at_once = 256 * (s.head_dim == 128 ? (pl->dtype == RC_F32 ? 2 : 3) : 4);
     const int64_t most = base <= kFewGroups ? std::min({ceil_div(blocks, 4), most_rows / (heads * rows), (int64_t)256}) : 1;
     const double read_us = (double)base * (double)blocks * (128.0 * s.head_dim) / 5.8e6;
