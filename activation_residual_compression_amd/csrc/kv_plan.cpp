@@ -84,7 +84,7 @@ Way way_of(const rc_kv_plan* pl, int64_t queries, int64_t blocks, bool chosen, i
     // parts, or for causal rows, whose parts differ and are started longest first, the
     // average and half the longest. Partial results cost a write and a read, and the
     // launch that joins them 1.5 steps. Measured in us, as it is and with one weight
-    // changed, over 30 calls, those that differ by more than 2 % most:
+    // changed, over 30 calls, the ones that change most:
     //   start and end 1   at 0: video share 699 and 718, fp32 2222 over 8000, 16 / 4 heads of
     //                     128, 290 and 304, 500 over 5000, 24 heads, 80 and 77; at 3: causal
     //                     512 over 8000, 24 heads of 128, 66 and 76, 3000 over 3000 64 and 48

@@ -147,8 +147,8 @@ rc_status_t rc_kv_select(rc_kv_plan_t plan, hipStream_t stream, const rc_kv_cach
 /* Attention: out = softmax(scale * q k^T) v over the tokens that each query sees
  * and, with `blocks` (as rc_kv_select lays them out; NULL: all), that lie in the
  * blocks chosen for its tile. A list ends at its first entry that is negative or not
- * below the number of blocks that the tile sees; entries may be
- * in any order, and the same block twice counts twice.
+ * below the number of blocks that the tile sees; entries may be in any order, and the
+ * same block twice counts twice.
  * out: [batch][queries][q_heads][head_dim] in the plan's dtype.
  * lse (NULL, or fp32 [batch][queries][q_heads]): the natural logarithm of the sum
  * of the exponentials, to join this result with attention over other tokens. A
