@@ -35,15 +35,11 @@
 namespace rc {
 namespace {
 
-constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kBias = 7.0f, kMost = 0x1p15f;  // f16 holds 2^15
 constexpr int kEvUp = 2, kEvDown = 8;
-constexpr float kLowest = -3.402823466e38f;
 // Rows of a block of threads of the kernel for many rows.
 template <int D, bool F32>
 constexpr int many_rows() { return D == 128 && F32 ? 32 : 64; }
-
-__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // The rows of a call: row r of key head h is query r / G, query head h * G + r % G.
 struct Row {
@@ -158,16 +154,6 @@ __device__ __forceinline__ u32x4 keep_codes(u32x4 u, int n) {
     u[i] &= mask;
   }
   return u;
-}
-
-// Two floats written to, read from, memory that every XCD sees.
-__device__ __forceinline__ void put_pair(float* p, float2 x) {
-  const uint64_t u = (uint64_t)__float_as_uint(x.y) << 32 | __float_as_uint(x.x);
-  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float2 get_pair(const float* p) {
-  const uint64_t u = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  return make_float2(__uint_as_float((uint32_t)u), __uint_as_float((uint32_t)(u >> 32)));
 }
 
 // The blocks that a wave reads, entries from, from + step, ... below to, one after the
@@ -494,12 +480,6 @@ __device__ __forceinline__ Place place_of(const KvAttendArgs& a, uint32_t w, uin
   }
   const int tile = (int)in_head / a.splits;
   return {(int)b, (int)h, (int)in_head % a.splits, a.causal ? row_tiles - 1 - tile : tile};
-}
-
-// The larger of a lane's value and that of the lane 32 away.
-__device__ __forceinline__ float max_halves(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 // One block of threads: 64 rows of one key head, a part of the keys; its four waves

@@ -67,4 +67,25 @@ __device__ __forceinline__ half8_t codes8(uint32_t a, uint32_t b) {
   return half8_t{w.x, w.y, x.x, x.y, y.x, y.y, z.x, z.y};
 }
 
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLowest = -3.402823466e38f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The larger of a lane's value and that of the lane 32 away.
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Two floats written to, read from, memory that every XCD sees.
+__device__ __forceinline__ void put_pair(float* p, float2 x) {
+  const uint64_t u = (uint64_t)__float_as_uint(x.y) << 32 | __float_as_uint(x.x);
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 get_pair(const float* p) {
+  const uint64_t u = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__uint_as_float((uint32_t)u), __uint_as_float((uint32_t)(u >> 32)));
+}
+
 }  // namespace rc

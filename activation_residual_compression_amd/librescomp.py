@@ -1,4 +1,4 @@
-"""ctypes binding of the librescomp C ABI (``include/librescomp.h``).
+"""ctypes binding of the librescomp C ABI (``include/librescomp*.h``).
 
 Argument marshalling only: every step of the compression path runs in the HIP
 kernels of ``librescomp.so``. Functions keep the C names; a non-RC_OK status
@@ -76,6 +76,23 @@ class rc_kv_view_t(ctypes.Structure):
                 ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
+RC_ATTN_MAX_PARTS = 8  # librescomp_attn.h
+RC_ATTN_CAUSAL = 1     # rc_attn_params_t.flags
+
+
+class rc_attn_shape_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("q_heads", "kv_heads", "head_dim", "max_seqs", "max_queries",
+                                              "max_keys")]
+
+
+class rc_attn_params_t(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class rc_pages_shape_t(ctypes.Structure):  # librescomp_pages.h
+    _fields_ = [(n, ctypes.c_int32) for n in ("slots", "kv_heads", "head_dim", "pool_blocks", "seq_blocks")]
+
+
 class RcError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -125,6 +142,25 @@ def _load():
     lib.rc_kv_plan_destroy.argtypes = [vp]
     lib.rc_kv_workspace_bytes.restype = sz
     lib.rc_kv_workspace_bytes.argtypes = [vp]
+    i = ctypes.c_int
+    lib.rc_attn_plan_create.argtypes = [rc_attn_shape_t, i, ctypes.POINTER(rc_attn_params_t), ctypes.POINTER(vp)]
+    lib.rc_attn_packed.argtypes = [vp, vp, i, vp, vp, i, i, i, i, view, view, view, view, vp]
+    lib.rc_attn_join.argtypes = [vp, i, view, ctypes.POINTER(vp), i, i, i, i, view, vp]
+    lib.rc_attn_plan_destroy.argtypes = [vp]
+    lib.rc_pages_plan_create.argtypes = [rc_pages_shape_t, ctypes.POINTER(vp)]
+    lib.rc_pages_reserve.argtypes = [vp, vp, cache, vp, vp, vp, vp, vp]
+    lib.rc_pages_fork.argtypes = [vp, vp, vp, vp, vp, vp]
+    lib.rc_pages_free.argtypes = [vp, vp, vp, vp, vp]
+    lib.rc_pages_compact.argtypes = [vp, vp, cache, vp, vp, vp, vp]
+    lib.rc_pages_copy.argtypes = [vp, vp, cache, cache, vp, vp, i]
+    lib.rc_pages_plan_destroy.argtypes = [vp]
+    for f in ("rc_attn_plan_create", "rc_attn_packed", "rc_attn_join", "rc_attn_plan_destroy", "rc_pages_plan_create",
+              "rc_pages_reserve", "rc_pages_fork", "rc_pages_free", "rc_pages_compact", "rc_pages_copy",
+              "rc_pages_plan_destroy"):
+        getattr(lib, f).restype = st
+    for f in ("rc_attn_workspace_bytes", "rc_pages_workspace_bytes"):
+        getattr(lib, f).restype = sz
+        getattr(lib, f).argtypes = [vp]
     lib.rc_status_string.restype = ctypes.c_char_p
     lib.rc_status_string.argtypes = [ctypes.c_int]
     lib.rcx_lowrank_workspace.restype = ctypes.c_int
@@ -584,6 +620,270 @@ class KvPlan:
     def close(self):
         if self.handle is not None:
             rc_kv_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+# ------------------------------------------------------------------ attention over packed sequences
+def rc_attn_plan_create(shape, dtype, params: rc_attn_params_t):
+    """shape: rc_attn_shape_t or its fields in order; dtype: enum int or name."""
+    if not isinstance(shape, rc_attn_shape_t):
+        shape = rc_attn_shape_t(*shape)
+    plan = ctypes.c_void_p()
+    _check(_lib.rc_attn_plan_create(shape, int(DTYPES.get(dtype, dtype)), ctypes.byref(params), ctypes.byref(plan)),
+           "rc_attn_plan_create")
+    return plan
+
+
+def rc_attn_packed(plan, stream, seqs, q_offsets, kv_offsets, q_tokens, kv_tokens, max_q, max_kv, q: rc_kv_view_t,
+                   k: rc_kv_view_t, v: rc_kv_view_t, out: rc_kv_view_t, lse):
+    _check(_lib.rc_attn_packed(plan, _stream(stream), int(seqs), _ptr(q_offsets), _ptr(kv_offsets), int(q_tokens),
+                               int(kv_tokens), int(max_q), int(max_kv), ctypes.byref(q), ctypes.byref(k),
+                               ctypes.byref(v), ctypes.byref(out), _ptr(lse)), "rc_attn_packed")
+
+
+def rc_attn_plan_destroy(plan):
+    _check(_lib.rc_attn_plan_destroy(plan), "rc_attn_plan_destroy")
+
+
+def rc_attn_workspace_bytes(plan) -> int:
+    return int(_lib.rc_attn_workspace_bytes(plan))
+
+
+def rc_attn_join(stream, outs, lses, batch, tokens, heads, head_dim, out: rc_kv_view_t, lse):
+    """outs: list of rc_kv_view_t; lses: list of device pointers."""
+    n = len(outs)
+    if len(lses) != n:
+        raise ValueError("%d outputs but %d log-sum-exps" % (n, len(lses)))
+    _check(_lib.rc_attn_join(_stream(stream), n, (rc_kv_view_t * n)(*outs), (ctypes.c_void_p * n)(*map(_ptr, lses)),
+                             int(batch), int(tokens), int(heads), int(head_dim), ctypes.byref(out), _ptr(lse)),
+           "rc_attn_join")
+
+
+_torch = _codes = None
+
+
+def _need_torch():
+    """torch, for the checks of the classes below (importing this module does not need it)."""
+    global _torch, _codes
+    if _torch is None:
+        import torch
+        _torch, _codes = torch, {torch.bfloat16: RC_BF16, torch.float32: RC_F32}
+    return _torch
+
+
+def _on_current(x, what):
+    """Refuses host tensors, and those of another device than the current one, whose stream and
+    memory the call uses."""
+    if not x.is_cuda:
+        raise ValueError("%s must be a device tensor" % what)
+    if x.get_device() != _torch._C._cuda_getDevice():
+        raise ValueError("%s is on device %d, the current one is %d" % (what, x.get_device(), _torch._C._cuda_getDevice()))
+
+
+def _array(x, n, what, dtype="int32"):
+    """Pointer of a contiguous device tensor of n values, None for None."""
+    if x is None:
+        return None
+    _on_current(x, what)
+    if x.dtype is not getattr(_torch, dtype) or not x.is_contiguous() or x.numel() != n:
+        raise ValueError("%s must be a contiguous %s device tensor of %d values" % (what, dtype, n))
+    return x.data_ptr()
+
+
+class AttnPlan:
+    """Owns one rc_attn_plan_t: attention of packed sequences over their own keys and values.
+    max_seqs, max_queries, max_keys: of a call, all sequences together."""
+
+    def __init__(self, q_heads, kv_heads, head_dim, dtype="bf16", max_seqs=1, max_queries=1, max_keys=1, causal=False,
+                 scale=0.0):
+        _need_torch()
+        self.handle = None
+        self.q_heads, self.kv_heads, self.head_dim = int(q_heads), int(kv_heads), int(head_dim)
+        self.dtype = DTYPES.get(dtype, dtype)
+        self.handle = rc_attn_plan_create((self.q_heads, self.kv_heads, self.head_dim, int(max_seqs), int(max_queries),
+                                           int(max_keys)), self.dtype,
+                                          rc_attn_params_t(float(scale), RC_ATTN_CAUSAL if causal else 0))
+        self.workspace_bytes = rc_attn_workspace_bytes(self.handle)
+
+    def _rows(self, x, tokens, heads, what):
+        _on_current(x, what)
+        if x.dim() != 3 or tuple(x.shape) != (tokens, heads, self.head_dim):
+            raise ValueError("%s is %s, the call takes (%d, %d, %d)" % (what, tuple(x.shape), tokens, heads, self.head_dim))
+        if _codes.get(x.dtype) != self.dtype:
+            raise ValueError("%s is %s, the plan takes %s" % (what, x.dtype, "bfloat16" if self.dtype == RC_BF16 else "float32"))
+        t, h, d = x.stride() if tokens else (heads * self.head_dim, self.head_dim, 1)  # torch's are any where nothing is
+        if d != 1:
+            raise ValueError("%s must have contiguous rows of head_dim" % what)
+        return rc_kv_view_t(x.data_ptr(), self.dtype, 0, t, h)
+
+    def attend(self, q, k, v, q_offsets, out, lse=None, kv_offsets=None, max_q=0, max_kv=0, stream=None):
+        """Attention of q [query tokens, q_heads, head_dim] over k, v [key tokens, kv_heads,
+        head_dim] of the same sequence; q_offsets (and kv_offsets, if the keys' differ): int32
+        [sequences + 1]. Writes out, like q, and lse, fp32 [query tokens, q_heads]. max_q, max_kv:
+        bounds of one sequence's lengths, if known."""
+        nq, nk = q.shape[0], k.shape[0]
+        views = (self._rows(q, nq, self.q_heads, "q"), self._rows(k, nk, self.kv_heads, "k"),
+                 self._rows(v, nk, self.kv_heads, "v"), self._rows(out, nq, self.q_heads, "out"))
+        seqs = q_offsets.numel() - 1
+        rc_attn_packed(self.handle, stream, seqs, _array(q_offsets, seqs + 1, "q_offsets"),
+                       _array(kv_offsets, seqs + 1, "kv_offsets"), nq, nk, max_q, max_kv, *views,
+                       _array(lse, nq * self.q_heads, "lse", "float32"))
+
+    def close(self):
+        if self.handle is not None:
+            rc_attn_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+def join_attention(outs, lses, out, lse=None, stream=None):
+    """Joins attentions of the same queries over different tokens (rc_attn_join): outs, tensors
+    [batch, tokens, heads, head_dim] or [tokens, heads, head_dim] of one dtype, with their lses,
+    fp32 of the shape without head_dim. Writes out, a tensor of that shape, bf16 or fp32, and lse.
+    They may be those of one of the parts."""
+    _need_torch()
+    shape = out.shape
+    if len(shape) not in (3, 4) or len(outs) != len(lses):
+        raise ValueError("out is %s, with %d outputs and %d log-sum-exps" % (tuple(shape), len(outs), len(lses)))
+    if out.numel() == 0:
+        return
+    views = []
+    for what, x in [("out", out)] + [("outs[%d]" % i, x) for i, x in enumerate(outs)]:
+        _on_current(x, what)
+        if x.shape != shape or x.dtype not in _codes:
+            raise ValueError("%s is %s %s, the call takes bfloat16 or float32 of %s" % (what, tuple(x.shape), x.dtype, tuple(shape)))
+        stride = x.stride()
+        if stride[-1] != 1:
+            raise ValueError("%s must have contiguous rows of head_dim" % what)
+        views.append(rc_kv_view_t(x.data_ptr(), _codes[x.dtype], stride[0] if len(shape) == 4 else 0, stride[-3], stride[-2]))
+    batch, (tokens, heads, dim) = shape[0] if len(shape) == 4 else 1, shape[-3:]
+    n = batch * tokens * heads
+    rc_attn_join(stream, views[1:], [_array(x, n, "lses[%d]" % i, "float32") for i, x in enumerate(lses)], batch, tokens,
+                 heads, dim, views[0], _array(lse, n, "lse", "float32"))
+
+
+# ------------------------------------------------------------------ pages of the cache
+def rc_pages_plan_create(shape):
+    """shape: rc_pages_shape_t or its fields in order."""
+    if not isinstance(shape, rc_pages_shape_t):
+        shape = rc_pages_shape_t(*shape)
+    plan = ctypes.c_void_p()
+    _check(_lib.rc_pages_plan_create(shape, ctypes.byref(plan)), "rc_pages_plan_create")
+    return plan
+
+
+def rc_pages_reserve(plan, stream, cache: rc_kv_cache_t, refs, table, start, tokens, missing):
+    _check(_lib.rc_pages_reserve(plan, _stream(stream), ctypes.byref(cache), _ptr(refs), _ptr(table), _ptr(start),
+                                 _ptr(tokens), _ptr(missing)), "rc_pages_reserve")
+
+
+def rc_pages_fork(plan, stream, refs, table, source, length):
+    _check(_lib.rc_pages_fork(plan, _stream(stream), _ptr(refs), _ptr(table), _ptr(source), _ptr(length)),
+           "rc_pages_fork")
+
+
+def rc_pages_free(plan, stream, refs, table, keep):
+    _check(_lib.rc_pages_free(plan, _stream(stream), _ptr(refs), _ptr(table), _ptr(keep)), "rc_pages_free")
+
+
+def rc_pages_compact(plan, stream, cache: rc_kv_cache_t, refs, table, used, moved):
+    _check(_lib.rc_pages_compact(plan, _stream(stream), ctypes.byref(cache), _ptr(refs), _ptr(table), _ptr(used),
+                                 _ptr(moved)), "rc_pages_compact")
+
+
+def rc_pages_copy(plan, stream, source: rc_kv_cache_t, to: rc_kv_cache_t, src, dst, count):
+    _check(_lib.rc_pages_copy(plan, _stream(stream), ctypes.byref(source), ctypes.byref(to), _ptr(src), _ptr(dst),
+                              int(count)), "rc_pages_copy")
+
+
+def rc_pages_plan_destroy(plan):
+    _check(_lib.rc_pages_plan_destroy(plan), "rc_pages_plan_destroy")
+
+
+def rc_pages_workspace_bytes(plan) -> int:
+    return int(_lib.rc_pages_workspace_bytes(plan))
+
+
+class PagePlan:
+    """Owns one rc_pages_plan_t: the blocks of a KvCache given out to `slots` sequences through
+    `table`, int32 [slots, seq_blocks], and counted in `refs`, int32 [pool_blocks]."""
+
+    def __init__(self, slots, kv_heads, head_dim, pool_blocks, seq_blocks):
+        _need_torch()
+        self.handle = None
+        self.slots, self.pool_blocks, self.seq_blocks = int(slots), int(pool_blocks), int(seq_blocks)
+        self.geometry = (self.pool_blocks, int(kv_heads), int(head_dim))
+        self.handle = rc_pages_plan_create((self.slots, int(kv_heads), int(head_dim), self.pool_blocks, self.seq_blocks))
+        self.workspace_bytes = rc_pages_workspace_bytes(self.handle)
+
+    def empty(self, device="cuda"):
+        """(refs, table) of a cache that no sequence uses."""
+        return (_torch.zeros(self.pool_blocks, dtype=_torch.int32, device=device),
+                _torch.full((self.slots, self.seq_blocks), -1, dtype=_torch.int32, device=device))
+
+    def _state(self, refs, table):
+        return _array(refs, self.pool_blocks, "refs"), _array(table, self.slots * self.seq_blocks, "table")
+
+    def _cache(self, cache):
+        if cache.geometry != self.geometry:
+            raise ValueError("the cache has (blocks, heads, head_dim) %s, the plan %s" % (cache.geometry, self.geometry))
+        _on_current(cache.k, "the cache")
+        return cache.struct
+
+    def reserve(self, cache, refs, table, start, tokens, missing=None, stream=None):
+        """Give every sequence s blocks of its own for tokens[s] new tokens from start[s] on; missing:
+        int32 [1], 0 or how many blocks are lacking (then nothing changes)."""
+        rc_pages_reserve(self.handle, stream, self._cache(cache), *self._state(refs, table),
+                         _array(start, self.slots, "start"), _array(tokens, self.slots, "tokens"),
+                         _array(missing, 1, "missing"))
+
+    def fork(self, refs, table, source, length, stream=None):
+        """Sequence s continues sequence source[s] (-1: stays) from its first length[s] tokens on."""
+        rc_pages_fork(self.handle, stream, *self._state(refs, table), _array(source, self.slots, "source"),
+                      _array(length, self.slots, "length"))
+
+    def free(self, refs, table, keep, stream=None):
+        """Keep the first keep[s] tokens of every sequence and give the blocks behind them back."""
+        rc_pages_free(self.handle, stream, *self._state(refs, table), _array(keep, self.slots, "keep"))
+
+    def compact(self, cache, refs, table, used=None, moved=None, stream=None):
+        """Move the blocks in use to the front of the pool; used: int32 [1], their number; moved: int32
+        [pool_blocks], each block's place now."""
+        rc_pages_compact(self.handle, stream, self._cache(cache), *self._state(refs, table), _array(used, 1, "used"),
+                         _array(moved, self.pool_blocks, "moved"))
+
+    def copy(self, cache, src, dst, to=None, stream=None):
+        """Copy block src[i] of the cache to block dst[i] of `to` (of the same cache by default)."""
+        source, count = self._cache(cache), src.numel()
+        rc_pages_copy(self.handle, stream, source, source if to is None else self._cache(to), _array(src, count, "src"),
+                      _array(dst, count, "dst"), count)
+
+    def close(self):
+        if self.handle is not None:
+            rc_pages_plan_destroy(self.handle)
             self.handle = None
 
     def __del__(self):
