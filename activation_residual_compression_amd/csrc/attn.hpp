@@ -26,6 +26,7 @@ struct AttnArgs {
   uint32_t* arrived;       // [groups of rows], zero between calls
 };
 hipError_t launch_attn_few(const AttnArgs& a, bool bf16, hipStream_t s);
+hipError_t launch_attn_many(const AttnArgs& a, int u, hipStream_t s);
 
 struct AttnJoinArgs {
   KvRows in[RC_ATTN_MAX_PARTS];

@@ -4,6 +4,7 @@
 
 #include <float.h>
 #include <math.h>
+#include <stdlib.h>
 
 #include <algorithm>
 #include <new>
@@ -43,7 +44,7 @@ Way way_of(const rc_attn_plan* pl, int64_t seqs, int64_t q_tokens, int64_t kv_to
   // Blocks of threads that the CUs hold at once.
   const int64_t at_once = 256 * (pl->dtype == RC_F32 ? 2 : 3);
   Way w{1, (int)std::max<int64_t>(max_kv, 1), 0};
-  if (base > kFewGroups || rows == 0) return w;
+  if (base > kFewGroups || rows == 0 || (pl->dtype == RC_BF16 && max_q * group > 64)) return w;
   // equal parts of all keys that are read, one for each block of threads
   const int64_t read = kv_tokens * s.kv_heads * groups;
   const int64_t chunk = std::max<int64_t>(256, ceil_div(ceil_div(read, at_once), 64) * 64);
@@ -163,6 +164,12 @@ rc_status_t rc_attn_packed(rc_attn_plan_t pl, hipStream_t stream, int seqs, cons
   a.part = static_cast<float*>(pl->ws);
   a.part_ml = reinterpret_cast<float2*>(a.part + w.part_rows * s.head_dim);
   a.arrived = pl->arrived;
+  const int64_t rows = (int64_t)a.max_q * a.group;
+  if (pl->dtype == RC_BF16 && rows > 16 && w.splits == 1) {
+    const char* e = getenv("RC_U");
+    const int u = e ? atoi(e) : (int64_t)q_tokens * a.group / 256 * a.kv_heads >= 200 ? 2 : 1;
+    return rc::launch_attn_many(a, u, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
+  }
   return rc::launch_attn_few(a, pl->dtype == RC_BF16, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
 }
 
