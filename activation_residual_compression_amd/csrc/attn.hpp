@@ -1,5 +1,5 @@
 // Internal interface of attention over packed sequences and of the join: what the host
-// code (attn_plan.cpp) hands to the kernel files attn_few / attn_join.
+// code (attn_plan.cpp) hands to the kernel files attn_few / attn_many / attn_join.
 #pragma once
 
 #include "../../include/librescomp_attn.h"
@@ -24,9 +24,12 @@ struct AttnArgs {
   float* part;
   float2* part_ml;
   uint32_t* arrived;       // [groups of rows], zero between calls
+  int4* joins;             // the kernel for many rows: [tiles of rows x key heads]: sequence, key head, tile, parts (0: one)
 };
 hipError_t launch_attn_few(const AttnArgs& a, bool bf16, hipStream_t s);
-hipError_t launch_attn_many(const AttnArgs& a, int u, hipStream_t s);
+// 128 u rows a block of threads, kg groups of waves for them; `chunk` counts tiles of 64 keys, and partial
+// results are [tile and head][part][rows of a tile][D]. grid: as many blocks as there can be parts.
+hipError_t launch_attn_many(const AttnArgs& a, int u, int kg, int64_t grid, hipStream_t s);
 
 struct AttnJoinArgs {
   KvRows in[RC_ATTN_MAX_PARTS];

@@ -31,9 +31,10 @@ __device__ __forceinline__ bool attn_part(const AttnArgs& a, int n, int split, i
 }
 
 // What a row's outputs are multiplied by at the end, and its log-sum-exp, from its maximum
-// in base 2 and its sum. Only a sum of zero is a row that sees nothing: NaN stays NaN.
+// in base 2 and its sum (1 or more but for roundings, or 0). Only a sum of zero is a row that sees
+// nothing: NaN stays NaN.
 __device__ __forceinline__ float attn_inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
-__device__ __forceinline__ float attn_lse(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2; }
+__device__ __forceinline__ float attn_lse(float m, float l) { return l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2; }
 
 __device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u; }
 

@@ -1,8 +1,10 @@
 // Attention over packed sequences, for many query rows, bf16.
 //
-// One block of threads: 4 waves of 32 U rows each of one key head of one sequence (row r:
-// query r / G, query head h * G + r % G), a part of the keys. Tiles of 64 keys and values go
-// through three LDS buffers that all waves share, one barrier a tile.
+// One block of threads: 128 U rows of one key head of one sequence (row r: query r / G, query head
+// h * G + r % G), a part of the keys. KG groups of four waves have the same rows, 32 U a wave, and
+// take every KG-th tile of 64 keys. A group's tiles go through two LDS buffers of 64 D x 4 bytes,
+// written past the registers while the other is read; one barrier a tile. Groups are joined in
+// LDS, parts by a second launch.
 //
 // S^T = K Q^T and O^T = V^T P^T: a lane holds scores of one row only (its column), the softmax
 // is in the lane, and its weights, rounded to bf16, are the second product's operand as they
@@ -14,7 +16,18 @@
 // weights of a step sum to more than 2^10, which the sum shows that is needed anyway, so the
 // accumulators are rescaled a few times in all, and no maximum is taken otherwise. bf16 and
 // fp32 hold such weights as well as those up to 1; both cancel in out = O / l.
+//
+// Bound by the matrix units and the power they may draw: a tile of 64 keys of a wave with 64 rows
+// is 64 (D 128) matrix instructions of 32 cycles, 2048 of the about 2900 cycles that two such waves
+// of a SIMD take for one of theirs each; the exponentials (8 cycles each, 512) and the LDS reads
+// run beside them. 8192 queries over 8192 keys, 32 heads of 128 on 8: 896 us, 1227 TFLOP/s (a
+// large matrix product of the library: 1251, at the 1.8 GHz that the card's power allows both);
+// 4444 over 17776, 30 heads of 64: 650 us, 933 TFLOP/s. U = 2 reads K and V from LDS once for 64
+// rows: with one row group a wave LDS bounds it (1087 us). KG = 2 is for calls of few tiles of
+// rows, where a CU would hold one block of four waves: 1152 over 4608, 2 x 24 heads of 128, 126
+// us, KG = 1 171.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_device.hpp"
 
@@ -27,14 +40,15 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kMost = 0x1p10f;
 constexpr int kTile = 64;
+constexpr int kMostParts = 16;  // of a tile of rows
 
 // A tile in LDS: rows of 2 D bytes without gaps, as the loads that write them lay them. The
-// 16-byte chunks of a row are in the order c ^ turn(row), so that a column of chunks (K, 16
-// rows a step of a read) or four rows of 32 bytes (V) meet different banks.
+// 16-byte chunks of a row are in the order c ^ turn(row), so that what a read takes in one cycle,
+// a column of 16 chunks (K) or four rows of 64 bytes (V), meets different banks.
 template <int D>
 __device__ __forceinline__ int k_turn(int row) { return D == 128 ? row & 15 : row >> 1 & 7; }
 template <int D>
-__device__ __forceinline__ int v_turn(int row) { return D == 128 ? (row & 7) << 1 : (row >> 1 & 3) << 1; }
+__device__ __forceinline__ int v_turn(int row) { return D == 128 ? (row & 3) << 2 : (row >> 1 & 1) << 2; }
 
 // 16 bytes a lane from memory into LDS at `to` (one for the wave) + 16 lane, past the
 // registers, from base + offset or from an address of each lane. The compiler's own form of this
@@ -47,29 +61,63 @@ __device__ __forceinline__ void load_lds(uint32_t to, const void* at) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(at) : "memory");
 }
 
-// Which rows a block of threads does. Tiles of rows are given out by their number from the
-// end of their sequence, highest first over all sequences: with a causal mask the long ones
-// first, and without it those of the long sequences.
+// vmcnt(0). In the form that the compiler understands: it would else go on waiting, tile after
+// tile, for loads from before the loop, and with them for the ones of load_lds.
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70);
+  asm volatile("" ::: "memory");
+}
+
+// The thread's number, as if not known yet: what is worked out from it anew, where it is needed,
+// takes no registers through the loops.
+__device__ __forceinline__ int thread_again() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
+// The sum of a lane's value and that of the lane 32 away.
+__device__ __forceinline__ float sum_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// x of the one lane `lane`.
+__device__ __forceinline__ AttnSeq of_lane(const AttnSeq& s, int lane) {
+  const auto of = [&](int x) { return __builtin_amdgcn_readlane(x, lane); };
+  return {of(s.q0), of(s.nq), of(s.k0), of(s.nk)};
+}
+
+// Sum of x over the wave's lanes, the same in all: inside rows of 16 lanes by moves between
+// neighbours, over the rows by scalars.
+__device__ __forceinline__ int wave_total(int x) {
+  x += (int)dpp_u32<kQuadXor1>((uint32_t)x);
+  x += (int)dpp_u32<kQuadXor2>((uint32_t)x);
+  x += (int)dpp_u32<kHalfMirror>((uint32_t)x);
+  x += (int)dpp_u32<kRowMirror>((uint32_t)x);
+  return __builtin_amdgcn_readlane(x, 0) + __builtin_amdgcn_readlane(x, 16) + __builtin_amdgcn_readlane(x, 32) + __builtin_amdgcn_readlane(x, 48);
+}
+__device__ __forceinline__ int wave_top(int x) {  // the largest, of numbers that are not negative
+  x = (int)group_max_u32<16>((uint32_t)x);
+  return max(max(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16)),
+             max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48)));
+}
+
+// Which rows a block of threads does; called by a whole wave. Tiles of rows are given out by
+// their number in their sequence, highest first over all sequences: with a causal mask the long
+// ones first, and without it those of the long sequences.
 struct Place {
   int b, h, tile;  // b < 0: none
 };
-__device__ __forceinline__ int tiles_of(const AttnArgs& a, int b, int rows_per) {
-  return (attn_seq(a, b).nq * a.group + rows_per - 1) / rows_per;
+__device__ __forceinline__ int tiles_of(const AttnArgs& a, const AttnSeq& s, int rows_per) {
+  return (s.nq * a.group + rows_per - 1) / rows_per;
 }
-__device__ __forceinline__ int wave_sum(int x) {
-#pragma unroll
-  for (int d = 32; d; d /= 2) x += __shfl_xor(x, d);
-  return x;
-}
-__device__ __forceinline__ int wave_max(int x) {
-#pragma unroll
-  for (int d = 32; d; d /= 2) x = max(x, __shfl_xor(x, d));
-  return x;
-}
-__device__ __forceinline__ Place place_of(const AttnArgs& a, uint32_t w, uint32_t grid, int rows_per) {
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ Place place_of(const AttnArgs& a, uint32_t w, uint32_t grid, int rows_per, AttnSeq& s) {
+  const int lane = thread_again() & 63;
   if (a.seqs == 1) {
-    const uint32_t tiles = (uint32_t)tiles_of(a, 0, rows_per);
+    s = attn_seq(a, 0);
+    const uint32_t tiles = (uint32_t)tiles_of(a, s, rows_per);
     uint32_t t, h;
     if (a.causal) {
       h = w % (uint32_t)a.kv_heads;
@@ -77,43 +125,58 @@ __device__ __forceinline__ Place place_of(const AttnArgs& a, uint32_t w, uint32_
     } else {  // blocks of threads go to the 8 XCDs in turn: each gets a run of the heads' tiles
       const uint32_t xcd = w & 7u;
       w = xcd * (grid >> 3) + min(xcd, grid & 7u) + (w >> 3);
-      t = w % tiles;
-      h = w / tiles;
+      t = w % max(tiles, 1u);
+      h = w / max(tiles, 1u);
     }
     if (t >= tiles || h >= (uint32_t)a.kv_heads) return {-1, 0, 0};
     return {0, (int)h, (int)(a.causal ? tiles - 1 - t : t)};
   }
   const int h = (int)(w % (uint32_t)a.kv_heads), t = (int)(w / (uint32_t)a.kv_heads);
-  // the level (number of a tile in its sequence) that holds the t-th tile from the top
-  int top = 0;
-  for (int b = lane; b < a.seqs; b += 64) top = max(top, tiles_of(a, b, rows_per));
-  int lo = 0, hi = wave_max(top);  // tiles at levels from lo on: more than t; from hi on: not
-  int above = 0;                   // tiles at levels from hi on
-  {
-    int n = 0;
-    for (int b = lane; b < a.seqs; b += 64) n += tiles_of(a, b, rows_per);
-    if (wave_sum(n) <= t) return {-1, 0, 0};
-  }
+  // a lane has the sequences lane, 64 + lane, ...: the first one's tiles are kept, others read again
+  s = attn_seq(a, min(lane, a.seqs - 1));
+  const int mine = lane < a.seqs ? tiles_of(a, s, rows_per) : 0;
+  const auto sum_over = [&](int level) {  // tiles at levels from `level` on
+    int n = max(mine - level, 0);
+    for (int b = lane + 64; b < a.seqs; b += 64) n += max(tiles_of(a, attn_seq(a, b), rows_per) - level, 0);
+    return wave_total(n);
+  };
+  if (sum_over(0) <= t) return {-1, 0, 0};
+  int top = mine;
+  for (int b = lane + 64; b < a.seqs; b += 64) top = max(top, tiles_of(a, attn_seq(a, b), rows_per));
+  // the level that holds the t-th tile from the top: from lo on there are more than t, from hi on not
+  int lo = 0, hi = wave_top(top), above = 0;  // above: tiles at levels from hi on
   while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    int n = 0;
-    for (int b = lane; b < a.seqs; b += 64) n += max(tiles_of(a, b, rows_per) - mid, 0);
-    n = wave_sum(n);
+    const int mid = (lo + hi) / 2, n = sum_over(mid);
     if (n > t) lo = mid;
     else hi = mid, above = n;
   }
   int rank = t - above;  // among the sequences that reach level lo
   for (int b0 = 0; b0 < a.seqs; b0 += 64) {
-    const int b = b0 + lane;
-    uint64_t reach = __ballot(b < a.seqs && tiles_of(a, min(b, a.seqs - 1), rows_per) > lo);
+    const AttnSeq own = b0 ? attn_seq(a, min(b0 + lane, a.seqs - 1)) : s;
+    uint64_t reach = __ballot(b0 + lane < a.seqs && tiles_of(a, own, rows_per) > lo);
     const int n = __builtin_popcountll(reach);
     if (rank < n) {
       for (; rank; --rank) reach &= reach - 1;
-      return {b0 + (int)__builtin_ctzll(reach), h, lo};
+      const int who = (int)__builtin_ctzll(reach);
+      s = of_lane(own, who);
+      return {b0 + who, h, lo};
     }
     rank -= n;
   }
   return {-1, 0, 0};
+}
+
+// Channels 4 half + 0..3 of two neighbouring groups of 8, x and y, as bf16: half 0 gets all 8 of x,
+// half 1 of y.
+__device__ __forceinline__ u32x4 rows_of_8(f32x4 x, f32x4 y) {
+  u32x4 w;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const auto z = __builtin_amdgcn_permlane32_swap(bf16_pair(x[2 * e], x[2 * e + 1]), bf16_pair(y[2 * e], y[2 * e + 1]), false, false);
+    w[e] = z[0];
+    w[2 + e] = z[1];
+  }
+  return w;
 }
 
 // Four keys of a lane's channel, from four rows of V in LDS.
@@ -121,37 +184,48 @@ __device__ __forceinline__ s16x4 read_turned(const char* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
 }
 
-template <int D, int U>
-__global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
+template <int D, int U, int KG>
+__global__ __launch_bounds__(256 * KG, 2) void attn_many_kernel(AttnArgs a) {
   constexpr int NK = D / 16, ND = D / 32, ROWS = 128 * U;
   constexpr int PER = D / 8, ROW = 2 * D, HALF = kTile * ROW, BYTES = 2 * HALF;  // chunks, bytes of a row; bytes of K, of a tile
   constexpr int C = D / 32, STEP = kTile / C;  // loads of a thread for a tile of K, and the rows between two of them
-  __shared__ __align__(1024) char shared[2 * BYTES];
-  __shared__ int strange;  // the last tile that held a value which is not finite and hidden from some row
-  const Place place = place_of(a, blockIdx.x, gridDim.x, ROWS);
-  const int b = __builtin_amdgcn_readfirstlane(place.b), h = __builtin_amdgcn_readfirstlane(place.h);
-  if (b < 0) return;
-  AttnSeq sq = attn_seq(a, b);
-  sq = {__builtin_amdgcn_readfirstlane(sq.q0), __builtin_amdgcn_readfirstlane(sq.nq), __builtin_amdgcn_readfirstlane(sq.k0),
-        __builtin_amdgcn_readfirstlane(sq.nk)};
-  const int rows = sq.nq * a.group, r0 = __builtin_amdgcn_readfirstlane(place.tile) * ROWS;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 31, half = lane >> 5;
+  __shared__ __align__(1024) char shared[KG * 2 * BYTES];
+  __shared__ float2 sml[KG == 1 ? 1 : 2][KG == 1 ? 1 : ROWS];
+  __shared__ int strange[KG];  // a group's last tile that held a value which is not finite and hidden from some row
+  const auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+  // The last parts of all tiles come first: only the long tiles have such.
+  const uint32_t all = gridDim.x / a.splits, w = blockIdx.x % all;
+  const int split = a.splits - 1 - (int)(blockIdx.x / all);
+  AttnSeq sq;
+  const Place place = place_of(a, w, all, ROWS, sq);
+  const int b = uniform(place.b), h = uniform(place.h), r0 = uniform(place.tile) * ROWS;
+  if (b < 0) {
+    if (a.splits > 1 && split == 0 && threadIdx.x == 0) a.joins[w].w = 0;
+    return;
+  }
+  sq = {uniform(sq.q0), uniform(sq.nq), uniform(sq.k0), uniform(sq.nk)};
+  const int rows = sq.nq * a.group;
   const int lim_lo = attn_limit(a, sq, r0 / a.group);
   const int lim_hi = attn_limit(a, sq, (min(r0 + ROWS, rows) - 1) / a.group);
-  const int tiles = (lim_hi + kTile - 1) / kTile;
-  if (tid == 0) strange = -1;
+  const int all_tiles = (lim_hi + kTile - 1) / kTile;
+  const int parts = min(max((all_tiles + a.chunk - 1) / a.chunk, 1), a.splits), per = (all_tiles + parts - 1) / parts;
+  if (a.splits > 1 && split == 0 && threadIdx.x == 0) a.joins[w] = make_int4(b, h, place.tile, parts > 1 ? parts : 0);
+  if (split >= parts) return;
+  const int from = min(split * per, all_tiles), tiles = min(from + per, all_tiles);  // up to `tiles`
+  const int tid = thread_again(), lane = tid & 63, col = lane & 31, half = lane >> 5;
+  const int wave = uniform(tid >> 6) & 3, group = KG == 1 ? 0 : uniform(tid >> 8);
+  char* const mine = shared + group * 2 * BYTES;
 
   // staging: load i of a thread has chunk lane % PER of row STEP i + srow, whose turn does not depend on i
   const char* const kh = (const char*)((const uint16_t*)a.k.data + (int64_t)sq.k0 * a.k.st + (int64_t)h * a.k.sh);
   const char* const vh = (const char*)((const uint16_t*)a.v.data + (int64_t)sq.k0 * a.v.st + (int64_t)h * a.v.sh);
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)shared;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)mine;
   const bool near = (a.k.st | a.v.st) < (int64_t)1 << 24;  // a tile's offsets fit 32 bits
-  const auto stage = [&](int tile) {
-    int again = threadIdx.x;  // what follows from it would take registers through the loop
-    asm volatile("" : "+v"(again));
-    const int lane = again & 63, srow = wave * (STEP / 4) + lane / PER;
+  const auto stage = [&](int tile, int buffer) {
+    if (tile >= tiles) return;
+    const int lane = thread_again() & 63, srow = wave * (STEP / 4) + lane / PER;
     const uint32_t k_turned = (uint32_t)((lane % PER) ^ k_turn<D>(srow)) * 16, v_turned = (uint32_t)((lane % PER) ^ v_turn<D>(srow)) * 16;
-    const uint32_t to = lds0 + (uint32_t)((tile & 1) * BYTES + wave * (STEP / 4) * ROW);
+    const uint32_t to = lds0 + (uint32_t)(buffer * BYTES + wave * (STEP / 4) * ROW);
     if (near && (tile + 1) * kTile <= sq.nk) {
       const uint32_t k_off = (uint32_t)srow * (uint32_t)(2 * a.k.st) + k_turned, v_off = (uint32_t)srow * (uint32_t)(2 * a.v.st) + v_turned;
 #pragma unroll
@@ -168,16 +242,16 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
       }
     }
   };
-  if (tiles > 0) stage(0);
+  stage(from + group, 0);
 
   // rows of this wave, and its queries: operand f has channels 16 f + 8 half + 0..7
   bf16x8 q[U][NK];
   float m_run[U], l_run[U];
-  int wave_lo = INT32_MAX, wave_hi = 0;  // what its rows see
+  int wave_lo = INT32_MAX, my_tiles = 0;  // keys that all its rows see, tiles that one does
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int r = r0 + 32 * U * wave + 32 * u + col, rr = min(r, rows - 1);
-    const uint16_t* p = (const uint16_t*)a.q.data + (int64_t)(sq.q0 + rr / a.group) * a.q.st + (int64_t)(h * a.group + rr % a.group) * a.q.sh;
+    const int r = min(r0 + 32 * U * wave + 32 * u + col, rows - 1);
+    const uint16_t* p = (const uint16_t*)a.q.data + (int64_t)(sq.q0 + r / a.group) * a.q.st + (int64_t)(h * a.group + r % a.group) * a.q.sh;
 #pragma unroll
     for (int f = 0; f < NK; ++f) q[u][f] = *reinterpret_cast<const bf16x8*>(p + 16 * f + 8 * half);
     m_run[u] = kLowest;
@@ -187,14 +261,11 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
     const int first = r0 + 32 * U * wave, last = min(first + 32 * U, rows) - 1;
     if (first < rows) {
       wave_lo = attn_limit(a, sq, first / a.group);
-      wave_hi = attn_limit(a, sq, last / a.group);
+      my_tiles = min((attn_limit(a, sq, last / a.group) + kTile - 1) / kTile, tiles);
     }
   }
-  const int my_tiles = (wave_hi + kTile - 1) / kTile;
   const auto limit = [&](int u) {  // keys that the lane's row sees
-    int again = threadIdx.x;
-    asm volatile("" : "+v"(again));
-    return attn_limit(a, sq, min(r0 + 32 * U * wave + 32 * u + (again & 31), rows - 1) / a.group);
+    return attn_limit(a, sq, min(r0 + 32 * U * wave + 32 * u + (thread_again() & 31), rows - 1) / a.group);
   };
   f32x16 o[U][ND];
 #pragma unroll
@@ -207,195 +278,358 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
   int k_at = col * ROW + (half ^ k_turn<D>(col)) * 16;
   int v_at = HALF + vrow * ROW + ((2 * (lane >> 4 & 1) + (lane & 3) / 2) ^ v_turn<D>(vrow)) * 16 + (lane & 1) * 8;
 
-  for (int t = 0; t < tiles; ++t) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's loads of tile t are in LDS
-    __syncthreads();                                  // the others' too, and tile t - 1 is read
-    if (t + 1 < tiles) stage(t + 1);
-    char* const tile = shared + (t & 1) * BYTES;
-    if ((t + 1) * kTile > lim_lo) {
-      // What is not finite among values that some row does not see is taken out of the product
-      // (zero times it is NaN) and added after it for the rows that see it.
-      int again = threadIdx.x;
-      asm volatile("" : "+v"(again));
-      const int lane = again & 63, srow = wave * (STEP / 4) + lane / PER;
-      bool odd = false;
-#pragma unroll 1
-      for (int i = 0; i < C; ++i) {
-        const int row = i * STEP + srow;
-        u32x4* at = reinterpret_cast<u32x4*>(tile + HALF + row * ROW + lane % PER * 16);
-        u32x4 x = *at;
-        bool here = false;
+  // operand f of K of the 32 keys whose rows begin at `tile`, and of their V: step at / ND of channels 32 (at % ND)
+  const auto key = [&](const char* tile, int f) { return *reinterpret_cast<const bf16x8*>(tile + (k_at ^ 32 * f)); };
+  const auto value = [&](const char* tile, int at) {
+    const char* v = tile + 16 * (at / ND) * ROW + (v_at ^ 64 * (at % ND));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(read_turned(v), read_turned(v + 8 * ROW), 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  const auto hide = [&](f32x16& s, int u, int first) {  // scores of keys from `first` on that the row does not see
+    if (first + 32 <= wave_lo) return;
+    // by bits, not by comparisons, whose 16 results at once would spill scalars
+    const int left = min(max(limit(u) - first - 4 * (thread_again() >> 5 & 1), 0), 31);  // the last bit, key 28, is the highest used
+    const uint32_t seen = (1u << left) - 1u;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const bool lo = (x[w] & 0x7F80u) == 0x7F80u, hi = (x[w] & 0x7F800000u) == 0x7F800000u;
-          here |= lo || hi;
-          x[w] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
-        }
-        if (here && t * kTile + row >= lim_lo) {
-          *at = x;
-          odd = true;
-        }
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t on = (uint32_t)((int32_t)(seen << (31 - 8 * (i / 4) - i % 4)) >> 31);
+      s[i] = __uint_as_float((__float_as_uint(s[i]) & on) | (0xFF800000u & ~on));
+    }
+  };
+  // weights i .. i + N - 1 of 32 keys
+  const auto weigh = [&](const f32x16& s, int u, int i, auto n, float& sum, u32x4 (&p)[2]) {
+    constexpr int N = decltype(n)::value;
+    float e[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) e[k] = exp2_fast(fmaf(s[i + k], a.scale, -m_run[u]));
+#pragma unroll
+    for (int k = 0; k < N; ++k) sum += e[k];
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+      uint32_t w = bf16_pair(e[k], e[k + 1]);
+      asm volatile("" : "+v"(w), "+v"(sum));  // in its place, or the compiler gathers all at the end
+      p[(i + k) / 8][(i + k) % 8 / 2] = w;
+    }
+  };
+  const auto weigh_all = [&](const f32x16& s, int u, float& sum, u32x4 (&p)[2]) {
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {  // four at a time, so that they take few registers
+      weigh(s, u, i, std::integral_constant<int, 4>{}, sum, p);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  const auto settle = [&](const f32x16& s, int u, float& sum, u32x4 (&p)[2]) {  // whether m has to rise
+    if (__any(sum > kMost)) {
+      float top = s[0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+      const float m_new = fmaxf(m_run[u], max_halves(top) * a.scale), alpha = exp2_fast(m_run[u] - m_new);
+      l_run[u] *= alpha;
+      m_run[u] = m_new;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[u][d][k] *= alpha;
+      weigh_all(s, u, sum, p);
+    }
+    l_run[u] += sum;
+  };
+  // A tile of keys. Two row groups: operands of K and V serve both, 32 keys at a time.
+  const auto shared_keys = [&](const char* tile, int first) {
+    asm volatile("" : "+v"(k_at), "+v"(v_at));  // or all their forms would be kept in registers
+    f32x16 s[U] = {};
+    u32x4 p[U][2];
+    float sum;
+    bf16x8 next = key(tile, 0);
+    if constexpr (D == 128) __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int f = 0; f < NK; ++f) {
+      const bf16x8 now = next;
+      if (f + 1 < NK) next = key(tile, f + 1);
+#pragma unroll
+      for (int u = 0; u < U; ++u) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now, q[u][f], s[u], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (D == 128) __builtin_amdgcn_s_setprio(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) hide(s[u], u, first);
+    next = value(tile, 0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      weigh_all(s[u], u, sum, p[u]);
+      settle(s[u], u, sum, p[u]);
+    }
+    if constexpr (D == 128) __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int at = 0; at < 2 * ND; ++at) {
+      const bf16x8 now = next;
+      if (at + 1 < 2 * ND) next = value(tile, at + 1);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        o[u][at % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now, __builtin_bit_cast(bf16x8, p[u][at / ND]), o[u][at % ND], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (D == 128) __builtin_amdgcn_s_setprio(0);
+  };
+  // One row group: the tile's two halves, the products of one beside the softmax of the other, two or four weights to
+  // a matrix instruction (8192 queries over 8192 keys, 16 heads of 128: 528 us, one after the other 543).
+  const auto in_turn = [&](const char* tile, int first) {
+    asm volatile("" : "+v"(k_at), "+v"(v_at));
+    const char* const tile_b = tile + 32 * ROW;
+    f32x16 sa = {}, sb = {};
+    u32x4 pa[2], pb[2];
+    float suma = 0.0f, sumb = 0.0f;
+    bf16x8 next = key(tile, 0);
+#pragma unroll
+    for (int f = 0; f < NK; ++f) {
+      const bf16x8 now = next;
+      next = f + 1 < NK ? key(tile, f + 1) : key(tile_b, 0);
+      sa = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now, q[0][f], sa, 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    hide(sa, 0, first);
+#pragma unroll
+    for (int f = 0; f < NK; ++f) {
+      sb = __builtin_amdgcn_mfma_f32_32x32x16_bf16(next, q[0][f], sb, 0, 0, 0);
+      if (f + 1 < NK) next = key(tile_b, f + 1);
+      weigh(sa, 0, 16 / NK * f, std::integral_constant<int, 16 / NK>{}, suma, pa);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    settle(sa, 0, suma, pa);
+    hide(sb, 0, first + 32);
+    next = value(tile, 0);
+#pragma unroll
+    for (int at = 0; at < 2 * ND; ++at) {
+      o[0][at % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(next, __builtin_bit_cast(bf16x8, pa[at / ND]), o[0][at % ND], 0, 0, 0);
+      next = at + 1 < 2 * ND ? value(tile, at + 1) : value(tile_b, 0);
+      weigh(sb, 0, 8 / ND * at, std::integral_constant<int, 8 / ND>{}, sumb, pb);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    settle(sb, 0, sumb, pb);
+#pragma unroll
+    for (int at = 0; at < 2 * ND; ++at) {
+      const bf16x8 now = next;
+      if (at + 1 < 2 * ND) next = value(tile_b, at + 1);
+      o[0][at % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now, __builtin_bit_cast(bf16x8, pb[at / ND]), o[0][at % ND], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // What is not finite among values that some row does not see is taken out of the product
+  // (zero times it is NaN) and added after it for the rows that see it.
+  const auto clear = [&](int t, char* tile) {
+    const int lane = thread_again() & 63, srow = wave * (STEP / 4) + lane / PER;
+    bool odd = false;
+#pragma unroll 1
+    for (int i = 0; i < C; ++i) {
+      const int row = i * STEP + srow;
+      u32x4* at = reinterpret_cast<u32x4*>(tile + HALF + row * ROW + lane % PER * 16);
+      u32x4 x = *at;
+      bool here = false;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const bool lo = (x[w] & 0x7F80u) == 0x7F80u, hi = (x[w] & 0x7F800000u) == 0x7F800000u;
+        here |= lo || hi;
+        x[w] = lo ? x[w] & 0xFFFF0000u : x[w];
+        x[w] = hi ? x[w] & 0xFFFFu : x[w];
       }
-      if (odd) strange = t;
+      if (here && t * kTile + row >= lim_lo) {
+        *at = x;
+        odd = true;
+      }
+    }
+    if (odd) strange[group] = t;
+  };
+  const auto add_strange = [&](int t) {
+    const int half = thread_again() >> 5 & 1;
+    int lim[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) lim[u] = limit(u);
+    for (int token = max(t * kTile, lim_lo); token < min((t + 1) * kTile, lim_hi); ++token) {
+      const uint16_t* v = (const uint16_t*)(vh + token * (2 * a.v.st));
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const u32x2 w = *reinterpret_cast<const u32x2*>(v + 32 * d + 8 * c + 4 * half);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = e % 2 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+            const float add = not_finite(y) ? y : 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) o[u][d][4 * c + e] += token < lim[u] ? add : 0.0f;
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+  };
+
+  if (thread_again() < KG) strange[thread_again()] = from - 1;
+  wait_loads();
+  for (int n = from; n < tiles; n += KG) {
+    const int t = n + group;
+    char* const tile = mine + ((n - from) / KG & 1) * BYTES;
+    wait_loads();     // this wave's of tile t are in LDS
+    __syncthreads();  // the others' too, and the last tile is read
+    stage(t + KG, ~((n - from) / KG) & 1);
+    if ((n + KG) * kTile > lim_lo) {
+      if (t < tiles) clear(t, tile);
       __syncthreads();
     }
     if (t >= my_tiles) continue;
-#pragma unroll
-    for (int hb = 0; hb < 2; ++hb) {
-      const int first = t * kTile + 32 * hb;  // key
-      asm volatile("" : "+v"(k_at), "+v"(v_at));  // or all their forms would be kept in registers
-      f32x16 s[U] = {};
-      {
-        const auto key = [&](int f) { return *reinterpret_cast<const bf16x8*>(tile + hb * 32 * ROW + (k_at ^ 32 * f)); };
-        bf16x8 kf = key(0);
-#pragma unroll
-        for (int f = 0; f < NK; ++f) {
-          const bf16x8 now = kf;
-          if (f + 1 < NK) kf = key(f + 1);
-#pragma unroll
-          for (int u = 0; u < U; ++u) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now, q[u][f], s[u], 0, 0, 0);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-      if (first + 32 > wave_lo) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          // by bits, not by comparisons, whose 32 results at once would spill scalars
-          const int left = min(max(limit(u) - first - 4 * half, 0), 31);  // the last bit, key 28, is the highest used
-          const uint32_t seen = (1u << left) - 1u;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t on = (uint32_t)((int32_t)(seen << (31 - 8 * (i / 4) - i % 4)) >> 31);
-            s[u][i] = __uint_as_float((__float_as_uint(s[u][i]) & on) | (0xFF800000u & ~on));
-          }
-        }
-      }
-      u32x4 ph[U][2];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const auto weigh = [&](float& sum) {
-          sum = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {  // four at a time, so that they take few registers
-            float p[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p[e] = exp2_fast(fmaf(s[u][i + e], a.scale, -m_run[u]));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum += p[e];
-            ph[u][i / 8][i % 8 / 2] = bf16_pair(p[0], p[1]);
-            ph[u][i / 8][i % 8 / 2 + 1] = bf16_pair(p[2], p[3]);
-            __builtin_amdgcn_sched_barrier(0);
-          }
-        };
-        float sum;
-        weigh(sum);
-        if (__any(sum > kMost)) {
-          float top = s[u][0];
-#pragma unroll
-          for (int i = 1; i < 16; ++i) top = fmaxf(top, s[u][i]);
-          const float m_new = fmaxf(m_run[u], max_halves(top) * a.scale), alpha = exp2_fast(m_run[u] - m_new);
-          l_run[u] *= alpha;
-          m_run[u] = m_new;
-#pragma unroll
-          for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[u][d][i] *= alpha;
-          weigh(sum);
-        }
-        l_run[u] += sum;
-      }
-      {
-        const auto value = [&](int at) {  // operand at % 2 of channels 32 (at / 2)
-          const char* v = tile + (32 * hb + 16 * (at % 2)) * ROW + (v_at ^ 64 * (at / 2));
-          return __builtin_bit_cast(bf16x8, __builtin_shufflevector(read_turned(v), read_turned(v + 8 * ROW), 0, 1, 2, 3, 4, 5, 6, 7));
-        };
-        bf16x8 vf = value(0);
-#pragma unroll
-        for (int at = 0; at < 2 * ND; ++at) {
-          const bf16x8 now = vf;
-          if (at + 1 < 2 * ND) vf = value(at + 1);
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            o[u][at / 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now, __builtin_bit_cast(bf16x8, ph[u][at % 2]), o[u][at / 2], 0, 0, 0);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
+    if constexpr (U == 1) {
+      in_turn(tile, t * kTile);
+    } else {
+      shared_keys(tile, t * kTile);
+      shared_keys(tile + 32 * ROW, t * kTile + 32);
     }
-    if (strange == t) {
-      int again = threadIdx.x;
-      asm volatile("" : "+v"(again));
-      const int half = again >> 5 & 1;
-      int lim[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) lim[u] = limit(u);
-      for (int token = max(t * kTile, lim_lo); token < min((t + 1) * kTile, lim_hi); ++token) {
-        const uint16_t* p = (const uint16_t*)(vh + token * (2 * a.v.st));
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(p + 32 * d + 8 * c + 4 * half);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float y = e % 2 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
-              const float add = not_finite(y) ? y : 0.0f;
-#pragma unroll
-              for (int u = 0; u < U; ++u) o[u][d][4 * c + e] += token < lim[u] ? add : 0.0f;
-            }
-            __builtin_amdgcn_sched_barrier(0);
-          }
-      }
-    }
+    if (strange[group] == t) add_strange(t);
   }
 
-  // the thread's place again, from its number alone: kept through the loop it would take registers
-  int again = threadIdx.x;
-  asm volatile("" : "+v"(again));
+  const int64_t slot = (int64_t)w * a.splits + split;  // of partial results
+  const int again = thread_again(), lane_ = again & 63, half_ = lane_ >> 5, row0 = 32 * U * wave + (lane_ & 31);
+#pragma unroll
+  for (int u = 0; u < U; ++u) l_run[u] = sum_halves(l_run[u]);
+  // With two groups either keeps half of the channels and hands over the others.
+  constexpr int NO = ND / KG;
+  f32x4* const give = reinterpret_cast<f32x4*>(shared + (KG - 1 - group) * (2 * BYTES)) + wave * (U * NO * 4 * 64) + lane_;
+  const f32x4* const take = reinterpret_cast<const f32x4*>(mine) + wave * (U * NO * 4 * 64) + lane_;
+  __syncthreads();  // LDS is read
+  if constexpr (KG == 2) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (half_ == 0) sml[group][row0 + 32 * u] = make_float2(m_run[u], l_run[u]);
+#pragma unroll
+      for (int d = 0; d < NO; ++d)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          f32x4 x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = group ? o[u][d][4 * c + e] : o[u][NO + d][4 * c + e];
+          give[((u * NO + d) * 4 + c) * 64] = x;
+        }
+    }
+    __syncthreads();
+  }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int col = again & 31, half = again >> 5 & 1;
-    const int r = r0 + 32 * U * wave + 32 * u + col;
-    const float l = l_run[u] + __shfl_xor(l_run[u], 32);
+    float m = m_run[u], l = l_run[u], f = 1.0f, g = 0.0f;
+    if constexpr (KG == 2) {
+      const float2 other = sml[1 - group][row0 + 32 * u];
+      m = fmaxf(m_run[u], other.x);
+      f = exp2_fast(m_run[u] - m);
+      g = exp2_fast(other.x - m);
+      l = l_run[u] * f + other.y * g;
+    }
+    const int r = r0 + row0 + 32 * u;
+    const bool live = r < rows;
+    f32x4* const part = reinterpret_cast<f32x4*>(a.part) + ((slot * (ROWS / 32) + wave * U + u) * ND + group * NO) * 4 * 64 + lane_;
     const float inv = attn_inverse(l);
     const int query = sq.q0 + r / a.group, head = h * a.group + r % a.group;
-    uint16_t* out = (uint16_t*)a.out.data + (int64_t)query * a.out.st + (int64_t)head * a.out.sh;
-    const bool live = r < rows;
+    uint16_t* const out = (uint16_t*)a.out.data + (int64_t)query * a.out.st + (int64_t)head * a.out.sh + group * (D / 2) + 8 * half_;
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+    for (int d = 0; d < NO; ++d)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        // this half has channels 4 half + 0..3 of groups of 8; after the exchange whole groups
-        u32x4 w;
+      for (int c = 0; c < 4; c += 2) {
+        f32x4 x[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t x = bf16_pair(o[u][d][8 * c + 2 * e] * inv, o[u][d][8 * c + 2 * e + 1] * inv);
-          const uint32_t y = bf16_pair(o[u][d][8 * c + 4 + 2 * e] * inv, o[u][d][8 * c + 4 + 2 * e + 1] * inv);
-          const auto z = __builtin_amdgcn_permlane32_swap(x, y, false, false);
-          w[e] = z[0];
-          w[2 + e] = z[1];
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[k][e] = KG == 2 && group ? o[u][ND - NO + d][4 * (c + k) + e] : o[u][d][4 * (c + k) + e];
+        if constexpr (KG == 2) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) x[k] = x[k] * f + take[((u * NO + d) * 4 + c + k) * 64] * g;
         }
-        if (live) *reinterpret_cast<u32x4*>(out + 32 * d + 16 * c + 8 * half) = w;
+        if (parts > 1) {  // as the lanes hold them
+          part[(d * 4 + c) * 64] = x[0];
+          part[(d * 4 + c + 1) * 64] = x[1];
+        } else {
+          const u32x4 w = rows_of_8(x[0] * inv, x[1] * inv);
+          if (live) *reinterpret_cast<u32x4*>(out + 32 * d + 8 * c) = w;
+        }
       }
-    if (live && half == 0 && a.lse) a.lse[(int64_t)query * a.q_heads + head] = attn_lse(m_run[u], l);
+    if (live && group == 0 && half_ == 0) {
+      if (parts > 1) a.part_ml[slot * ROWS + row0 + 32 * u] = make_float2(m, l);
+      else if (a.lse) a.lse[(int64_t)query * a.q_heads + head] = attn_lse(m, l);
+    }
   }
 }
 
-template <int D, int U>
-hipError_t run(const AttnArgs& a, hipStream_t s) {
-  // as many tiles of rows as the sequences can have: they end in the middle of one each
-  const int64_t rows = (int64_t)a.q_tokens * a.group, per = 128 * U;
-  const int64_t tiles = std::min(rows / per + a.seqs, a.seqs * (((int64_t)a.max_q * a.group + per - 1) / per));
-  const int64_t grid = tiles * a.kv_heads;
+// ------------------------------------------------------------------ joining parts
+// The parts of one tile of rows, in their order. A wave has 32 channels of 32 rows, its lanes what
+// they had in the kernel that wrote the parts; (m, l) of all parts are loaded at once, and outputs
+// of four parts, as each load waits for memory behind the last-level cache (1.5 us).
+template <int D, int ROWS>
+__global__ __launch_bounds__(256) void attn_many_join_kernel(AttnArgs a) {
+  constexpr int ND = D / 32, WAVES = ROWS / 32 * ND;  // of a tile
+  const int64_t j = blockIdx.x / (WAVES / 4);
+  const int4 join = a.joins[j];
+  if (join.w == 0) return;
+  const int lane = threadIdx.x & 63, half = lane >> 5, wave = blockIdx.x % (WAVES / 4) * 4 + (threadIdx.x >> 6);
+  const int set = wave / ND, d = wave % ND, in_tile = 32 * set + (lane & 31), h = join.y, parts = join.w;
+  const AttnSeq sq = attn_seq(a, join.x);
+  const int rows = sq.nq * a.group, r = join.z * ROWS + in_tile;
+  if (join.z * ROWS + 32 * set >= rows) return;
+  const int64_t slot = j * a.splits;
+  float2 ml[kMostParts];
+  float m = kLowest, l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kMostParts; ++i) ml[i] = a.part_ml[(slot + min(i, parts - 1)) * ROWS + in_tile];
+#pragma unroll
+  for (int i = 0; i < kMostParts; ++i) m = fmaxf(m, ml[i].x);
+  const f32x4* const y = reinterpret_cast<const f32x4*>(a.part) + ((slot * (ROWS / 32) + set) * ND + d) * 4 * 64 + lane;
+  constexpr int64_t STEP = (int64_t)ROWS * D / 4;  // from part to part
+  f32x4 x[4] = {};
+#pragma unroll
+  for (int i0 = 0; i0 < kMostParts; i0 += 4) {
+    if (i0 >= parts) break;
+    f32x4 z[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) z[i][c] = y[min(i0 + i, parts - 1) * STEP + c * 64];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i0 + i >= parts) break;
+      const float f = exp2_fast(ml[i0 + i].x - m);
+      l += ml[i0 + i].y * f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] += z[i][c] * f;
+    }
+  }
+  const float inv = attn_inverse(l);
+  const bool live = r < rows;
+  const int query = sq.q0 + r / a.group, hq = h * a.group + r % a.group;
+  uint16_t* out = (uint16_t*)a.out.data + (int64_t)query * a.out.st + (int64_t)hq * a.out.sh + 32 * d + 8 * half;
+#pragma unroll
+  for (int c = 0; c < 4; c += 2) {
+    const u32x4 w = rows_of_8(x[c] * inv, x[c + 1] * inv);
+    if (live) *reinterpret_cast<u32x4*>(out + 8 * c) = w;
+  }
+  if (live && half == 0 && d == 0 && a.lse) a.lse[(int64_t)query * a.q_heads + hq] = attn_lse(m, l);
+}
+
+template <int D, int U, int KG>
+hipError_t run(const AttnArgs& a, int64_t grid, hipStream_t s) {
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  attn_many_kernel<D, U><<<(unsigned)grid, 256, 0, s>>>(a);
-  return hipGetLastError();
+  attn_many_kernel<D, U, KG><<<(unsigned)grid, 256 * KG, 0, s>>>(a);
+  hipError_t err = hipGetLastError();
+  if (err == hipSuccess && a.splits > 1) {
+    attn_many_join_kernel<D, 128 * U><<<(unsigned)(grid / a.splits) * (U * D / 32), 256, 0, s>>>(a);
+    err = hipGetLastError();
+  }
+  return err;
+}
+
+template <int D>
+hipError_t pick(const AttnArgs& a, int u, int kg, int64_t grid, hipStream_t s) {
+  if (kg == 1) return u == 1 ? run<D, 1, 1>(a, grid, s) : run<D, 2, 1>(a, grid, s);
+  return u == 1 ? run<D, 1, 2>(a, grid, s) : run<D, 2, 2>(a, grid, s);
 }
 
 }  // namespace
 
-hipError_t launch_attn_many(const AttnArgs& a, int u, hipStream_t s) {
-  if (a.dim == 64) return u == 1 ? run<64, 1>(a, s) : run<64, 2>(a, s);
-  return u == 1 ? run<128, 1>(a, s) : run<128, 2>(a, s);
+hipError_t launch_attn_many(const AttnArgs& a, int u, int kg, int64_t grid, hipStream_t s) {
+  return a.dim == 64 ? pick<64>(a, u, kg, grid, s) : pick<128>(a, u, kg, grid, s);
 }
 
 }  // namespace rc

@@ -4,7 +4,6 @@
 
 #include <float.h>
 #include <math.h>
-#include <stdlib.h>
 
 #include <algorithm>
 #include <new>
@@ -19,7 +18,7 @@ struct rc_attn_plan {
   void* ws = nullptr;  // partial results: outputs, (m, l); then the counters
   size_t ws_bytes = 0;
   int64_t part_rows = 0;        // rows of partial results that it holds
-  uint32_t* arrived = nullptr;  // [kFewGroups]
+  uint32_t* arrived = nullptr;  // [kFewGroups], for the kernel for few rows
 };
 
 namespace {
@@ -28,36 +27,131 @@ using rc::at4;
 using rc::ceil_div;
 using rc::rows_of;
 
-// Groups of rows that may have several parts, at most.
+// Groups of rows of the kernel for few rows that may have several parts, at most.
 constexpr int64_t kFewGroups = 1536;
 
+// How a call runs: the kernel, its form, and in how many parts at most a group of rows reads
+// its keys, of which length (keys; tiles of 64 keys in the kernel for many rows).
 struct Way {
+  bool few;
+  int u, kg;
+  int64_t grid;
   int splits, chunk;
   int64_t part_rows;  // rows of partial results; 0 with one part
 };
 
-Way way_of(const rc_attn_plan* pl, int64_t seqs, int64_t q_tokens, int64_t kv_tokens, int64_t max_q, int64_t max_kv,
-           int64_t most_rows) {
+struct Call {
+  int64_t seqs, q_tokens, kv_tokens, max_q, max_kv, group;
+};
+
+// The kernel for few rows: 16 rows a block of threads.
+Way few_way(const rc_attn_plan* pl, const Call& c, int64_t most_rows) {
   const rc_attn_shape_t& s = pl->shape;
-  const int64_t group = s.q_heads / s.kv_heads, rows = q_tokens * s.q_heads;
-  const int64_t groups = ceil_div(max_q * group, 16), base = seqs * s.kv_heads * groups;
+  const int64_t rows = c.q_tokens * s.q_heads, groups = ceil_div(c.max_q * c.group, 16), base = c.seqs * s.kv_heads * groups;
   // Blocks of threads that the CUs hold at once.
   const int64_t at_once = 256 * (pl->dtype == RC_F32 ? 2 : 3);
-  Way w{1, (int)std::max<int64_t>(max_kv, 1), 0};
-  if (base > kFewGroups || rows == 0 || (pl->dtype == RC_BF16 && max_q * group > 64)) return w;
+  Way w{true, 0, 0, 0, 1, (int)std::max<int64_t>(c.max_kv, 1), 0};
+  if (base > kFewGroups || rows == 0) return w;
   // equal parts of all keys that are read, one for each block of threads
-  const int64_t read = kv_tokens * s.kv_heads * groups;
+  const int64_t read = c.kv_tokens * s.kv_heads * groups;
   const int64_t chunk = std::max<int64_t>(256, ceil_div(ceil_div(read, at_once), 64) * 64);
-  const int64_t splits = std::min({ceil_div(max_kv, chunk), most_rows / rows, (int64_t)256});
+  const int64_t splits = std::min({ceil_div(c.max_kv, chunk), most_rows / rows, (int64_t)256});
   if (splits <= 1) return w;
   w.splits = (int)splits;
-  w.chunk = (int)std::max(chunk, ceil_div(ceil_div(max_kv, splits), 64) * 64);
+  w.chunk = (int)std::max(chunk, ceil_div(ceil_div(c.max_kv, splits), 64) * 64);
   w.part_rows = splits * rows;
   return w;
 }
 
+// The kernel for many rows, in its four forms: 128 u rows a block of threads, kg groups of waves
+// that share its keys. `turn` is the time in us of a turn (64 keys for each group) with 1, 2, ...
+// blocks on a CU, as many as it holds; `start` a block's beginning and end; `join` the second
+// launch and `move` a megabyte of partial results, written and read. Fitted to 2800 measured calls
+// (180 shapes of 65 to 71000 rows, 200 to 17776 keys, 2 to 24 key heads, causal and not, each in
+// every form and in 1 to 16 parts), root mean square error 6 to 8 %; the form and number of parts
+// that it picks take 1.025 times as long as the best on average. For example, us: 1152 queries over
+// 4608 keys, 2 x 24 heads of 128: u 2, kg 2, one part 126; u 2, kg 1 171 (146 in two parts); u 1,
+// kg 1 144. 4444 over 17776, 30 heads of 64: u 2, kg 1 in 4 parts 667, in one 790. 8192 over 8192,
+// 32 / 8 heads of 128: u 2, kg 1 900, kg 2 950, u 1 1087. 200 over 200, 16 x 4 / 16 heads of 128:
+// u 1, kg 1 18, u 2 21.
+struct Form {
+  int u, kg, held;
+  double turn[4], start, join, move;
+};
+constexpr Form kForms128[] = {{1, 1, 2, {1.46, 1.85}, 6.2, 4.4, 0.10},
+                              {2, 1, 2, {2.05, 2.90}, 8.8, 3.6, 0.116},
+                              {1, 2, 1, {1.90}, 6.9, 5.2, 0.10},
+                              {2, 2, 1, {2.82}, 10.8, 4.3, 0.13}};
+constexpr Form kForms64[] = {{1, 1, 4, {0.95, 1.27, 1.61, 1.94}, 4.2, 5.1, 0.106},
+                             {2, 1, 3, {1.46, 2.02, 2.63}, 5.4, 5.5, 0.10},
+                             {1, 2, 2, {1.16, 1.99}, 5.4, 5.5, 0.088},
+                             {2, 2, 1, {2.01}, 6.7, 6.1, 0.108}};
+
+double cost_of(const rc_attn_plan* pl, const Call& c, const Form& f, int64_t parts) {
+  const rc_attn_shape_t& s = pl->shape;
+  const bool causal = (pl->params.flags & RC_ATTN_CAUSAL) != 0;
+  const double rows = 128.0 * f.u, n = (double)c.seqs;
+  const double tiles = std::min(n * (double)ceil_div(c.max_q * c.group, 128 * f.u), (double)(c.q_tokens * c.group) / rows + 0.5 * n);
+  const int64_t longest = ceil_div(c.max_kv, 64), chunk = ceil_div(longest, parts);
+  // A tile's keys on average, in tiles of 64, and in how many parts they are read. Long sequences have more
+  // tiles: half way from the average length to the longest.
+  const auto length = [&](int64_t tokens, int64_t most) { return 0.5 * ((double)tokens / n + (double)std::min(most, tokens)); };
+  double mean = length(c.kv_tokens, c.max_kv) / 64.0, cut = (double)parts;
+  if (causal) {
+    mean = std::max(mean - length(c.q_tokens, c.max_q) / 128.0, 0.5);
+    cut = parts > 1 ? 1.0 + std::max(0.0, mean / (double)chunk - 0.5) : 1.0;
+  }
+  const double blocks = tiles * s.kv_heads * cut, turns = (double)ceil_div(chunk, f.kg), full = 256.0 * f.held;
+  const auto turn = [&](double on_cu) { return f.turn[std::min(std::max((int)ceil(on_cu), 1), f.held) - 1]; };
+  const auto round = [&](double blocks_at_once) { return turns * turn(blocks_at_once / 256.0) + f.start; };
+  double us;
+  if (blocks <= (causal ? 0.5 : 1.0) * full) {
+    us = round(blocks);
+  } else if (causal) {  // long ones first: the longest, or all of them and half of one at the end
+    const double each = std::max(mean / cut / f.kg, 0.5) * f.turn[f.held - 1];
+    us = std::max(turns * turn(std::min(blocks, full) / 256.0) + f.start, blocks / full * (each + f.start) + 0.5 * each);
+  } else {  // whole rounds, and one of what is left
+    const double rounds = floor(blocks / full), left = blocks - rounds * full;
+    us = rounds * round(full) + (left > 0.0 ? round(left) : 0.0);
+  }
+  if (parts > 1) us = us * (causal ? 1.05 : 1.0) + f.join + f.move * blocks * rows * s.head_dim * 8e-6;
+  return us;
+}
+
+Way many_way(const rc_attn_plan* pl, const Call& c, int64_t most_rows) {
+  const rc_attn_shape_t& s = pl->shape;
+  Way best{};
+  double least = 0.0;
+  for (const Form& f : s.head_dim == 128 ? kForms128 : kForms64) {
+    const int64_t per = 128 * f.u;  // as many tiles of rows as there can be: a sequence ends inside of one
+    const int64_t tiles = std::min(c.q_tokens * c.group / per + c.seqs, c.seqs * ceil_div(c.max_q * c.group, per)) * s.kv_heads;
+    for (const int64_t parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (parts > 1 && (parts * 4 > ceil_div(c.max_kv, 64) || tiles * parts * per > most_rows)) break;
+      const double us = cost_of(pl, c, f, parts);
+      if (least > 0.0 && us >= least) continue;
+      least = us;
+      best = {false, f.u, f.kg, tiles * parts, (int)parts, (int)std::max<int64_t>(ceil_div(ceil_div(c.max_kv, 64), parts), 1),
+              parts > 1 ? tiles * parts * per : 0};
+    }
+  }
+  return best;
+}
+
+Way way_of(const rc_attn_plan* pl, const Call& c, int64_t most_rows) {
+  const int64_t rows = c.max_q * c.group;
+  // The kernel for few reads K and V once for each 16 rows, that for many has a larger tile than rows and a second
+  // launch for a join. Measured in us, few and many, rows 17, 32 and 64: 8 heads of 128, 2000 keys (8 MB) 15 and 18, 16
+  // and 18, 17 and 18; 24 heads (25 MB) 20 and 20, 20 and 20, 27 and 20; 8 heads of 64, 2000 keys (4 MB) 12 and 14, 12
+  // and 15, 13 and 16; 24 heads (12 MB) 13 and 15, 14 and 15, 17 and 16; 16 sequences (66 MB) 30 and 23, 30 and 22,
+  // 51 and 23: equal where 40 MB are read.
+  const int64_t reads = ceil_div(rows, 16) * c.kv_tokens * pl->shape.kv_heads * pl->shape.head_dim * 4;
+  const bool few = rows <= 16 || (rows <= 64 && reads <= (int64_t)40 << 20);
+  return pl->dtype == RC_BF16 && !few ? many_way(pl, c, most_rows) : few_way(pl, c, most_rows);
+}
+
+// Bytes of partial results: outputs, (m, l), and for each 128 rows or more which tile they are.
 size_t part_bytes(const rc_attn_plan* pl, int64_t part_rows) {
-  return (size_t)part_rows * ((size_t)pl->shape.head_dim * 4 + sizeof(float2));
+  return (size_t)part_rows * ((size_t)pl->shape.head_dim * 4 + sizeof(float2)) + (size_t)ceil_div(part_rows, 128) * sizeof(int4);
 }
 
 // Rows of partial results that the workspace is made for: what calls of one sequence, of
@@ -65,11 +159,11 @@ size_t part_bytes(const rc_attn_plan* pl, int64_t part_rows) {
 // gigabyte. A call that would need more takes fewer parts.
 int64_t part_rows_at_most(const rc_attn_plan* pl) {
   const rc_attn_shape_t& s = pl->shape;
-  const int64_t cap = ((int64_t)512 << 20) / (int64_t)part_bytes(pl, 1);
+  const int64_t cap = ((int64_t)512 << 20) / ((int64_t)s.head_dim * 4 + 9), group = s.q_heads / s.kv_heads;
   int64_t most = 0;
   for (int64_t n = 1;; n = std::min<int64_t>(2 * n, s.max_seqs)) {
     for (int64_t q = 1;; q = std::min<int64_t>(2 * q, s.max_queries)) {
-      if (q >= n) most = std::max(most, way_of(pl, n, q, s.max_keys, ceil_div(q, n), s.max_keys, cap).part_rows);
+      if (q >= n) most = std::max(most, way_of(pl, {n, q, s.max_keys, ceil_div(q, n), s.max_keys, group}, cap).part_rows);
       if (q == s.max_queries) break;
     }
     if (n == s.max_seqs) return most;
@@ -158,18 +252,14 @@ rc_status_t rc_attn_packed(rc_attn_plan_t pl, hipStream_t stream, int seqs, cons
   a.causal = (pl->params.flags & RC_ATTN_CAUSAL) != 0;
   constexpr float kLog2e = 1.44269504088896340736f;
   a.scale = fminf((pl->params.scale > 0.0f ? pl->params.scale : 1.0f / sqrtf((float)s.head_dim)) * kLog2e, FLT_MAX);
-  const Way w = way_of(pl, seqs, q_tokens, kv_tokens, a.max_q, a.max_kv, pl->part_rows);
+  const Way w = way_of(pl, {seqs, q_tokens, kv_tokens, a.max_q, a.max_kv, a.group}, pl->part_rows);
   a.splits = w.splits;
   a.chunk = w.chunk;
   a.part = static_cast<float*>(pl->ws);
   a.part_ml = reinterpret_cast<float2*>(a.part + w.part_rows * s.head_dim);
+  a.joins = reinterpret_cast<int4*>(a.part_ml + w.part_rows);
   a.arrived = pl->arrived;
-  const int64_t rows = (int64_t)a.max_q * a.group;
-  if (pl->dtype == RC_BF16 && rows > 16 && w.splits == 1) {
-    const char* e = getenv("RC_U");
-    const int u = e ? atoi(e) : (int64_t)q_tokens * a.group / 256 * a.kv_heads >= 200 ? 2 : 1;
-    return rc::launch_attn_many(a, u, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
-  }
+  if (!w.few) return rc::launch_attn_many(a, w.u, w.kg, w.grid, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
   return rc::launch_attn_few(a, pl->dtype == RC_BF16, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
 }
 

@@ -71,7 +71,9 @@ rc_status_t rc_attn_plan_create(rc_attn_shape_t shape, rc_dtype_t dtype, const r
  * exponentials. A query that sees no key, or whose scores are all -infinity, gets 0 and
  * -infinity.
  * Precision: scores, sums, the running maximum and outputs are held in fp32 and rounded
- * once.
+ * once. In bf16 the weights may be rounded to bf16 (8 bits) for their product with v, not
+ * for their sum: before the last rounding an output is within 2^-8 of the weighted mean of
+ * |v|.
  * NaN and infinities: what a query does not see does not reach it, whatever it holds. A
  * NaN among the queries, or the keys that one sees, or a score of +infinity makes its
  * outputs and lse NaN; a value that is not finite makes the outputs that see it not finite. */
