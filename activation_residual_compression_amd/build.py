@@ -25,7 +25,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["quant.hip", "nm.hip", "lowrank.hip", "blocksel.hip", "checks.hip", "noalloc.hip", "probe.hip", "plan.cpp",
            "kv_store.hip", "kv_select.hip", "kv_attend.hip", "kv_plan.cpp",
-           "attn_few.hip", "attn_many.hip", "attn_join.hip", "attn_plan.cpp", "pages.hip", "pages_plan.cpp"]
+           "attn_few.hip", "attn_many.hip", "attn_many_f32.hip",
+           "attn_join.hip", "attn_plan.cpp", "pages.hip", "pages_plan.cpp"]
 ARCH = os.environ.get("RC_OFFLOAD_ARCH", "gfx950")
 FLAGS = [
     "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",

@@ -25,11 +25,14 @@ struct AttnArgs {
   float2* part_ml;
   uint32_t* arrived;       // [groups of rows], zero between calls
   int4* joins;             // the kernel for many rows: [tiles of rows x key heads]: sequence, key head, tile, parts (0: one)
+  uint16_t* halves;        // fp32, the kernel for many rows: K and V as f16, [K1, K2, V1, V2][kv_heads][kv_tokens][D],
+  float* powers;           //   and their factors [kv_heads][K, V][kv_tokens]
 };
 hipError_t launch_attn_few(const AttnArgs& a, bool bf16, hipStream_t s);
 // 128 u rows a block of threads, kg groups of waves for them; `chunk` counts tiles of 64 keys, and partial
 // results are [tile and head][part][rows of a tile][D]. grid: as many blocks as there can be parts.
 hipError_t launch_attn_many(const AttnArgs& a, int u, int kg, int64_t grid, hipStream_t s);
+hipError_t launch_attn_many_f32(const AttnArgs& a, int64_t grid, hipStream_t s);  // the same, u = kg = 1
 
 struct AttnJoinArgs {
   KvRows in[RC_ATTN_MAX_PARTS];

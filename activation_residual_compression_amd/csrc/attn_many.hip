@@ -29,160 +29,14 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "attn_device.hpp"
+#include "attn_many.hpp"
 
 namespace rc {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
 constexpr float kMost = 0x1p10f;
-constexpr int kTile = 64;
-constexpr int kMostParts = 16;  // of a tile of rows
-
-// A tile in LDS: rows of 2 D bytes without gaps, as the loads that write them lay them. The
-// 16-byte chunks of a row are in the order c ^ turn(row), so that what a read takes in one cycle,
-// a column of 16 chunks (K) or four rows of 64 bytes (V), meets different banks.
-template <int D>
-__device__ __forceinline__ int k_turn(int row) { return D == 128 ? row & 15 : row >> 1 & 7; }
-template <int D>
-__device__ __forceinline__ int v_turn(int row) { return D == 128 ? (row & 3) << 2 : (row >> 1 & 1) << 2; }
-
-// 16 bytes a lane from memory into LDS at `to` (one for the wave) + 16 lane, past the
-// registers, from base + offset or from an address of each lane. The compiler's own form of this
-// makes every later read of LDS wait for it; here the wait is the caller's (vmcnt), once a tile.
-// Nothing else in these kernels uses m0.
-__device__ __forceinline__ void load_lds(uint32_t to, uint32_t offset, const void* base) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
-}
-__device__ __forceinline__ void load_lds(uint32_t to, const void* at) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(at) : "memory");
-}
-
-// vmcnt(0). In the form that the compiler understands: it would else go on waiting, tile after
-// tile, for loads from before the loop, and with them for the ones of load_lds.
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0F70);
-  asm volatile("" ::: "memory");
-}
-
-// The thread's number, as if not known yet: what is worked out from it anew, where it is needed,
-// takes no registers through the loops.
-__device__ __forceinline__ int thread_again() {
-  int t = threadIdx.x;
-  asm volatile("" : "+v"(t));
-  return t;
-}
-
-// The sum of a lane's value and that of the lane 32 away.
-__device__ __forceinline__ float sum_halves(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-
-// x of the one lane `lane`.
-__device__ __forceinline__ AttnSeq of_lane(const AttnSeq& s, int lane) {
-  const auto of = [&](int x) { return __builtin_amdgcn_readlane(x, lane); };
-  return {of(s.q0), of(s.nq), of(s.k0), of(s.nk)};
-}
-
-// Sum of x over the wave's lanes, the same in all: inside rows of 16 lanes by moves between
-// neighbours, over the rows by scalars.
-__device__ __forceinline__ int wave_total(int x) {
-  x += (int)dpp_u32<kQuadXor1>((uint32_t)x);
-  x += (int)dpp_u32<kQuadXor2>((uint32_t)x);
-  x += (int)dpp_u32<kHalfMirror>((uint32_t)x);
-  x += (int)dpp_u32<kRowMirror>((uint32_t)x);
-  return __builtin_amdgcn_readlane(x, 0) + __builtin_amdgcn_readlane(x, 16) + __builtin_amdgcn_readlane(x, 32) + __builtin_amdgcn_readlane(x, 48);
-}
-__device__ __forceinline__ int wave_top(int x) {  // the largest, of numbers that are not negative
-  x = (int)group_max_u32<16>((uint32_t)x);
-  return max(max(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16)),
-             max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48)));
-}
-
-// Which rows a block of threads does; called by a whole wave. Tiles of rows are given out by
-// their number in their sequence, highest first over all sequences: with a causal mask the long
-// ones first, and without it those of the long sequences.
-struct Place {
-  int b, h, tile;  // b < 0: none
-};
-__device__ __forceinline__ int tiles_of(const AttnArgs& a, const AttnSeq& s, int rows_per) {
-  return (s.nq * a.group + rows_per - 1) / rows_per;
-}
-__device__ __forceinline__ Place place_of(const AttnArgs& a, uint32_t w, uint32_t grid, int rows_per, AttnSeq& s) {
-  const int lane = thread_again() & 63;
-  if (a.seqs == 1) {
-    s = attn_seq(a, 0);
-    const uint32_t tiles = (uint32_t)tiles_of(a, s, rows_per);
-    uint32_t t, h;
-    if (a.causal) {
-      h = w % (uint32_t)a.kv_heads;
-      t = w / (uint32_t)a.kv_heads;
-    } else {  // blocks of threads go to the 8 XCDs in turn: each gets a run of the heads' tiles
-      const uint32_t xcd = w & 7u;
-      w = xcd * (grid >> 3) + min(xcd, grid & 7u) + (w >> 3);
-      t = w % max(tiles, 1u);
-      h = w / max(tiles, 1u);
-    }
-    if (t >= tiles || h >= (uint32_t)a.kv_heads) return {-1, 0, 0};
-    return {0, (int)h, (int)(a.causal ? tiles - 1 - t : t)};
-  }
-  const int h = (int)(w % (uint32_t)a.kv_heads), t = (int)(w / (uint32_t)a.kv_heads);
-  // a lane has the sequences lane, 64 + lane, ...: the first one's tiles are kept, others read again
-  s = attn_seq(a, min(lane, a.seqs - 1));
-  const int mine = lane < a.seqs ? tiles_of(a, s, rows_per) : 0;
-  const auto sum_over = [&](int level) {  // tiles at levels from `level` on
-    int n = max(mine - level, 0);
-    for (int b = lane + 64; b < a.seqs; b += 64) n += max(tiles_of(a, attn_seq(a, b), rows_per) - level, 0);
-    return wave_total(n);
-  };
-  if (sum_over(0) <= t) return {-1, 0, 0};
-  int top = mine;
-  for (int b = lane + 64; b < a.seqs; b += 64) top = max(top, tiles_of(a, attn_seq(a, b), rows_per));
-  // the level that holds the t-th tile from the top: from lo on there are more than t, from hi on not
-  int lo = 0, hi = wave_top(top), above = 0;  // above: tiles at levels from hi on
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2, n = sum_over(mid);
-    if (n > t) lo = mid;
-    else hi = mid, above = n;
-  }
-  int rank = t - above;  // among the sequences that reach level lo
-  for (int b0 = 0; b0 < a.seqs; b0 += 64) {
-    const AttnSeq own = b0 ? attn_seq(a, min(b0 + lane, a.seqs - 1)) : s;
-    uint64_t reach = __ballot(b0 + lane < a.seqs && tiles_of(a, own, rows_per) > lo);
-    const int n = __builtin_popcountll(reach);
-    if (rank < n) {
-      for (; rank; --rank) reach &= reach - 1;
-      const int who = (int)__builtin_ctzll(reach);
-      s = of_lane(own, who);
-      return {b0 + who, h, lo};
-    }
-    rank -= n;
-  }
-  return {-1, 0, 0};
-}
-
-// Channels 4 half + 0..3 of two neighbouring groups of 8, x and y, as bf16: half 0 gets all 8 of x,
-// half 1 of y.
-__device__ __forceinline__ u32x4 rows_of_8(f32x4 x, f32x4 y) {
-  u32x4 w;
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const auto z = __builtin_amdgcn_permlane32_swap(bf16_pair(x[2 * e], x[2 * e + 1]), bf16_pair(y[2 * e], y[2 * e + 1]), false, false);
-    w[e] = z[0];
-    w[2 + e] = z[1];
-  }
-  return w;
-}
-
-// Four keys of a lane's channel, from four rows of V in LDS.
-__device__ __forceinline__ s16x4 read_turned(const char* p) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
-}
 
 template <int D, int U, int KG>
 __global__ __launch_bounds__(256 * KG, 2) void attn_many_kernel(AttnArgs a) {
@@ -554,67 +408,13 @@ __global__ __launch_bounds__(256 * KG, 2) void attn_many_kernel(AttnArgs a) {
   }
 }
 
-// ------------------------------------------------------------------ joining parts
-// The parts of one tile of rows, in their order. A wave has 32 channels of 32 rows, its lanes what
-// they had in the kernel that wrote the parts; (m, l) of all parts are loaded at once, and outputs
-// of four parts, as each load waits for memory behind the last-level cache (1.5 us).
-template <int D, int ROWS>
-__global__ __launch_bounds__(256) void attn_many_join_kernel(AttnArgs a) {
-  constexpr int ND = D / 32, WAVES = ROWS / 32 * ND;  // of a tile
-  const int64_t j = blockIdx.x / (WAVES / 4);
-  const int4 join = a.joins[j];
-  if (join.w == 0) return;
-  const int lane = threadIdx.x & 63, half = lane >> 5, wave = blockIdx.x % (WAVES / 4) * 4 + (threadIdx.x >> 6);
-  const int set = wave / ND, d = wave % ND, in_tile = 32 * set + (lane & 31), h = join.y, parts = join.w;
-  const AttnSeq sq = attn_seq(a, join.x);
-  const int rows = sq.nq * a.group, r = join.z * ROWS + in_tile;
-  if (join.z * ROWS + 32 * set >= rows) return;
-  const int64_t slot = j * a.splits;
-  float2 ml[kMostParts];
-  float m = kLowest, l = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kMostParts; ++i) ml[i] = a.part_ml[(slot + min(i, parts - 1)) * ROWS + in_tile];
-#pragma unroll
-  for (int i = 0; i < kMostParts; ++i) m = fmaxf(m, ml[i].x);
-  const f32x4* const y = reinterpret_cast<const f32x4*>(a.part) + ((slot * (ROWS / 32) + set) * ND + d) * 4 * 64 + lane;
-  constexpr int64_t STEP = (int64_t)ROWS * D / 4;  // from part to part
-  f32x4 x[4] = {};
-#pragma unroll
-  for (int i0 = 0; i0 < kMostParts; i0 += 4) {
-    if (i0 >= parts) break;
-    f32x4 z[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) z[i][c] = y[min(i0 + i, parts - 1) * STEP + c * 64];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i0 + i >= parts) break;
-      const float f = exp2_fast(ml[i0 + i].x - m);
-      l += ml[i0 + i].y * f;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] += z[i][c] * f;
-    }
-  }
-  const float inv = attn_inverse(l);
-  const bool live = r < rows;
-  const int query = sq.q0 + r / a.group, hq = h * a.group + r % a.group;
-  uint16_t* out = (uint16_t*)a.out.data + (int64_t)query * a.out.st + (int64_t)hq * a.out.sh + 32 * d + 8 * half;
-#pragma unroll
-  for (int c = 0; c < 4; c += 2) {
-    const u32x4 w = rows_of_8(x[c] * inv, x[c + 1] * inv);
-    if (live) *reinterpret_cast<u32x4*>(out + 8 * c) = w;
-  }
-  if (live && half == 0 && d == 0 && a.lse) a.lse[(int64_t)query * a.q_heads + hq] = attn_lse(m, l);
-}
-
 template <int D, int U, int KG>
 hipError_t run(const AttnArgs& a, int64_t grid, hipStream_t s) {
   if (grid > INT32_MAX) return hipErrorInvalidValue;
   attn_many_kernel<D, U, KG><<<(unsigned)grid, 256 * KG, 0, s>>>(a);
   hipError_t err = hipGetLastError();
   if (err == hipSuccess && a.splits > 1) {
-    attn_many_join_kernel<D, 128 * U><<<(unsigned)(grid / a.splits) * (U * D / 32), 256, 0, s>>>(a);
+    attn_many_join_kernel<D, 128 * U, false><<<(unsigned)(grid / a.splits) * (U * D / 32), 256, 0, s>>>(a);
     err = hipGetLastError();
   }
   return err;

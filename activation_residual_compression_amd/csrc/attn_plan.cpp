@@ -19,6 +19,8 @@ struct rc_attn_plan {
   size_t ws_bytes = 0;
   int64_t part_rows = 0;        // rows of partial results that it holds
   uint32_t* arrived = nullptr;  // [kFewGroups], for the kernel for few rows
+  void* halves = nullptr;       // fp32: K and V of a call as f16, and their factors
+  bool many = false;            // whether the kernel for many rows can run
 };
 
 namespace {
@@ -39,6 +41,8 @@ struct Way {
   int splits, chunk;
   int64_t part_rows;  // rows of partial results; 0 with one part
 };
+
+size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 struct Call {
   int64_t seqs, q_tokens, kv_tokens, max_q, max_kv, group;
@@ -87,6 +91,9 @@ constexpr Form kForms64[] = {{1, 1, 4, {0.95, 1.27, 1.61, 1.94}, 4.2, 5.1, 0.106
                              {1, 2, 2, {1.16, 1.99}, 5.4, 5.5, 0.088},
                              {2, 2, 1, {2.01}, 6.7, 6.1, 0.108}};
 
+// fp32, its one form, of 128 and of 64: 16 heads, 4096 keys and 256, 512 (and 768) blocks of threads.
+constexpr Form kFormsF32[] = {{1, 1, 2, {3.57, 6.02}, 6.0, 8.0, 0.12}, {1, 1, 3, {2.48, 3.64, 5.01}, 5.0, 8.0, 0.12}};
+
 double cost_of(const rc_attn_plan* pl, const Call& c, const Form& f, int64_t parts) {
   const rc_attn_shape_t& s = pl->shape;
   const bool causal = (pl->params.flags & RC_ATTN_CAUSAL) != 0;
@@ -122,7 +129,10 @@ Way many_way(const rc_attn_plan* pl, const Call& c, int64_t most_rows) {
   const rc_attn_shape_t& s = pl->shape;
   Way best{};
   double least = 0.0;
-  for (const Form& f : s.head_dim == 128 ? kForms128 : kForms64) {
+  const bool f32 = pl->dtype == RC_F32, wide = s.head_dim == 128;
+  const Form* const forms = f32 ? &kFormsF32[wide ? 0 : 1] : wide ? kForms128 : kForms64;
+  for (int i = 0; i < (f32 ? 1 : 4); ++i) {
+    const Form& f = forms[i];
     const int64_t per = 128 * f.u;  // as many tiles of rows as there can be: a sequence ends inside of one
     const int64_t tiles = std::min(c.q_tokens * c.group / per + c.seqs, c.seqs * ceil_div(c.max_q * c.group, per)) * s.kv_heads;
     for (const int64_t parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
@@ -146,8 +156,22 @@ Way way_of(const rc_attn_plan* pl, const Call& c, int64_t most_rows) {
   // 51 and 23: equal where 40 MB are read.
   const int64_t reads = ceil_div(rows, 16) * c.kv_tokens * pl->shape.kv_heads * pl->shape.head_dim * 4;
   const bool few = rows <= 16 || (rows <= 64 && reads <= (int64_t)40 << 20);
-  return pl->dtype == RC_BF16 && !few ? many_way(pl, c, most_rows) : few_way(pl, c, most_rows);
+  if (pl->dtype == RC_F32) {
+    // The kernel for many splits K and V before, in a launch of its own. Few and many, us: 128 rows, 2000 keys, 8 heads
+    // of 64 (65 MB) 17 and 27; 256 rows (131 MB) 23 and 29; 512 rows (262 MB) 34 and 30; 256 rows, 8 heads of 128 (262
+    // MB) 41 and 36; 128 rows, 200 keys, 16 x 8 heads of 64 (210 MB) 24 and 25; with half of a tile or less 64 rows,
+    // 2000 keys, 16 x 8 heads of 128 (1 GB) 153 and 163.
+    return rows <= 64 || 2 * reads <= (int64_t)200 << 20 || !pl->many ? few_way(pl, c, most_rows) : many_way(pl, c, most_rows);
+  }
+  return few ? few_way(pl, c, most_rows) : many_way(pl, c, most_rows);
 }
+
+// Bytes of K and V of `keys` tokens as two f16 each, and of their factors.
+size_t half_bytes(const rc_attn_plan* pl, int64_t keys) {
+  return (size_t)keys * pl->shape.kv_heads * ((size_t)pl->shape.head_dim * 8 + 8);
+}
+// The kernel for many rows of fp32 is there for plans whose K and V as halves take no more than this.
+constexpr size_t kMostHalves = (size_t)4 << 30;
 
 // Bytes of partial results: outputs, (m, l), and for each 128 rows or more which tile they are.
 size_t part_bytes(const rc_attn_plan* pl, int64_t part_rows) {
@@ -198,14 +222,20 @@ rc_status_t rc_attn_plan_create(rc_attn_shape_t shape, rc_dtype_t dtype, const r
   pl->shape = shape;
   pl->dtype = dtype;
   pl->params = *params;
+  const size_t halves = half_bytes(pl, shape.max_keys);
+  pl->many = dtype == RC_BF16 || halves <= kMostHalves;
   pl->part_rows = part_rows_at_most(pl);
-  if (pl->part_rows) {
-    const size_t parts = part_bytes(pl, pl->part_rows), counts = kFewGroups * sizeof(uint32_t);
-    if (hipMalloc(&pl->ws, parts + counts) != hipSuccess) {
+  const size_t parts = pl->part_rows ? part_bytes(pl, pl->part_rows) : 0, counts = parts ? kFewGroups * sizeof(uint32_t) : 0;
+  const bool halved = dtype == RC_F32 && pl->many && (int64_t)shape.max_queries * (shape.q_heads / shape.kv_heads) > 64;
+  pl->ws_bytes = up16(parts + counts) + (halved ? halves : 0);
+  if (pl->ws_bytes) {
+    if (hipMalloc(&pl->ws, pl->ws_bytes) != hipSuccess) {
       delete pl;
       return RC_ERR_HIP;
     }
-    pl->ws_bytes = parts + counts;
+    if (halved) pl->halves = static_cast<char*>(pl->ws) + up16(parts + counts);
+  }
+  if (counts) {
     pl->arrived = reinterpret_cast<uint32_t*>(static_cast<char*>(pl->ws) + parts);
     // done before the first call, which may be on a stream that does not wait for this one
     if (hipMemset(pl->arrived, 0, counts) != hipSuccess || hipStreamSynchronize(nullptr) != hipSuccess) {
@@ -259,6 +289,11 @@ rc_status_t rc_attn_packed(rc_attn_plan_t pl, hipStream_t stream, int seqs, cons
   a.part_ml = reinterpret_cast<float2*>(a.part + w.part_rows * s.head_dim);
   a.joins = reinterpret_cast<int4*>(a.part_ml + w.part_rows);
   a.arrived = pl->arrived;
+  if (!w.few && pl->dtype == RC_F32) {
+    a.halves = static_cast<uint16_t*>(pl->halves);
+    a.powers = reinterpret_cast<float*>(a.halves + (int64_t)4 * s.kv_heads * kv_tokens * s.head_dim);
+    return rc::launch_attn_many_f32(a, w.grid, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
+  }
   if (!w.few) return rc::launch_attn_many(a, w.u, w.kg, w.grid, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
   return rc::launch_attn_few(a, pl->dtype == RC_BF16, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
 }
