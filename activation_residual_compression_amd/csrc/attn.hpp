@@ -28,7 +28,8 @@ struct AttnArgs {
   uint16_t* halves;        // fp32, the kernel for many rows: K and V as f16, [K1, K2, V1, V2][kv_heads][kv_tokens][D],
   float* powers;           //   and their factors [kv_heads][K, V][kv_tokens]
 };
-hipError_t launch_attn_few(const AttnArgs& a, bool bf16, hipStream_t s);
+// waves: 4, or more with one part; pieces: groups of 16 rows and parts of them, of a key head, at most.
+hipError_t launch_attn_few(const AttnArgs& a, bool bf16, int waves, int64_t pieces, hipStream_t s);
 // 128 u rows a block of threads, kg groups of waves for them; `chunk` counts tiles of 64 keys, and partial
 // results are [tile and head][part][rows of a tile][D]. grid: as many blocks as there can be parts.
 hipError_t launch_attn_many(const AttnArgs& a, int u, int kg, int64_t grid, hipStream_t s);

@@ -20,10 +20,10 @@ __device__ __forceinline__ int attn_limit(const AttnArgs& a, const AttnSeq& s, i
   return a.causal ? max(0, s.nk - s.nq + i + 1) : s.nk;
 }
 
-// The part of n keys that this block of threads reads; parts: of how many. Parts begin at
-// multiples of 64 keys.
-__device__ __forceinline__ bool attn_part(const AttnArgs& a, int n, int split, int& parts, int& from, int& to) {
-  parts = min(max((n + a.chunk - 1) / a.chunk, 1), a.splits);
+// The part of n keys that this block of threads reads; parts: of how many, `most` at most. Parts begin
+// at multiples of 64 keys.
+__device__ __forceinline__ bool attn_part(const AttnArgs& a, int n, int split, int most, int& parts, int& from, int& to) {
+  parts = min(max((n + a.chunk - 1) / a.chunk, 1), most);
   const int per = ((n + parts - 1) / parts + 63) & ~63;
   from = min(split * per, n);
   to = min(from + per, n);

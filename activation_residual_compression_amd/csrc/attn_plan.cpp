@@ -48,22 +48,28 @@ struct Call {
   int64_t seqs, q_tokens, kv_tokens, max_q, max_kv, group;
 };
 
-// The kernel for few rows: 16 rows a block of threads.
+// The kernel for few rows: 16 rows a block of threads of u waves.
 Way few_way(const rc_attn_plan* pl, const Call& c, int64_t most_rows) {
   const rc_attn_shape_t& s = pl->shape;
   const int64_t rows = c.q_tokens * s.q_heads, groups = ceil_div(c.max_q * c.group, 16), base = c.seqs * s.kv_heads * groups;
-  // Blocks of threads that the CUs hold at once.
-  const int64_t at_once = 256 * (pl->dtype == RC_F32 ? 2 : 3);
-  Way w{true, 0, 0, 0, 1, (int)std::max<int64_t>(c.max_kv, 1), 0};
+  const int64_t at_once = 512;  // blocks of threads that the CUs hold
+  Way w{true, 4, 0, c.seqs * groups, 1, (int)std::max<int64_t>(c.max_kv, 1), 0};
+  // Few short sequences: twice as many waves and no parts (333 tokens, 24 heads of 128: 8.1 us, two parts 10.3;
+  // 600 tokens, 32 heads on 8: 10.2, three parts 8.5).
+  if (base <= 256 && c.max_kv <= 512) {
+    w.u = 8;
+    return w;
+  }
   if (base > kFewGroups || rows == 0) return w;
-  // equal parts of all keys that are read, one for each block of threads
+  // equal parts of all keys that are read, one for each block of threads; each group's last part is half of one on average
   const int64_t read = c.kv_tokens * s.kv_heads * groups;
-  const int64_t chunk = std::max<int64_t>(256, ceil_div(ceil_div(read, at_once), 64) * 64);
+  const int64_t chunk = std::max<int64_t>(256, ceil_div(ceil_div(read, std::max(at_once - base / 2, at_once / 2)), 64) * 64);
   const int64_t splits = std::min({ceil_div(c.max_kv, chunk), most_rows / rows, (int64_t)256});
   if (splits <= 1) return w;
   w.splits = (int)splits;
   w.chunk = (int)std::max(chunk, ceil_div(ceil_div(c.max_kv, splits), 64) * 64);
   w.part_rows = splits * rows;
+  w.grid = groups * std::min(c.seqs * splits, c.kv_tokens / w.chunk + c.seqs);
   return w;
 }
 
@@ -295,7 +301,7 @@ rc_status_t rc_attn_packed(rc_attn_plan_t pl, hipStream_t stream, int seqs, cons
     return rc::launch_attn_many_f32(a, w.grid, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
   }
   if (!w.few) return rc::launch_attn_many(a, w.u, w.kg, w.grid, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
-  return rc::launch_attn_few(a, pl->dtype == RC_BF16, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
+  return rc::launch_attn_few(a, pl->dtype == RC_BF16, w.u, w.grid, stream) == hipSuccess ? RC_OK : RC_ERR_HIP;
 }
 
 rc_status_t rc_attn_plan_destroy(rc_attn_plan_t pl) {
