@@ -156,12 +156,12 @@ Way many_way(const rc_attn_plan* pl, const Call& c, int64_t most_rows) {
 Way way_of(const rc_attn_plan* pl, const Call& c, int64_t most_rows) {
   const int64_t rows = c.max_q * c.group;
   // The kernel for few reads K and V once for each 16 rows, that for many has a larger tile than rows and a second
-  // launch for a join. Measured in us, few and many, rows 17, 32 and 64: 8 heads of 128, 2000 keys (8 MB) 15 and 18, 16
-  // and 18, 17 and 18; 24 heads (25 MB) 20 and 20, 20 and 20, 27 and 20; 8 heads of 64, 2000 keys (4 MB) 12 and 14, 12
-  // and 15, 13 and 16; 24 heads (12 MB) 13 and 15, 14 and 15, 17 and 16; 16 sequences (66 MB) 30 and 23, 30 and 22,
-  // 51 and 23: equal where 40 MB are read.
+  // launch for a join. Measured in us, few and many, by what few reads: 8 heads of 128, 2000 keys, 64 rows (33 MB) 14
+  // and 19, 256 rows (131 MB) 21 and 22; 24 heads, 64 rows (98 MB) 20 and 21, 128 rows (197 MB) 31 and 23; 24 heads of
+  // 64, 2000 keys, 96 rows (74 MB) 15 and 18, 128 rows (98 MB) 20 and 18; 16 sequences of 500 keys, 32 rows (98 MB) 16
+  // and 16, 48 rows (147 MB) 22 and 18; 64 sequences of 200 keys, 8 heads of 128, 17 rows (105 MB) 20 and 18.
   const int64_t reads = ceil_div(rows, 16) * c.kv_tokens * pl->shape.kv_heads * pl->shape.head_dim * 4;
-  const bool few = rows <= 16 || (rows <= 64 && reads <= (int64_t)40 << 20);
+  const bool few = rows <= 16 || reads <= (int64_t)100 << 20;
   if (pl->dtype == RC_F32) {
     // The kernel for many splits K and V before, in a launch of its own. Few and many, us: 128 rows, 2000 keys, 8 heads
     // of 64 (65 MB) 17 and 27; 256 rows (131 MB) 23 and 29; 512 rows (262 MB) 34 and 30; 256 rows, 8 heads of 128 (262

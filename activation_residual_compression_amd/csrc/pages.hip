@@ -50,7 +50,9 @@ constexpr int kChunk = 16384;
 __host__ __device__ __forceinline__ int chunks_of(const PageGeom& g) {
   return (g.bytes[0] + kChunk - 1) / kChunk + (g.bytes[1] + kChunk - 1) / kChunk;
 }
-// Copies chunk `chunk` of block src to block dst; 256 threads.
+// Copies chunk `chunk` of block src to block dst; 256 threads. The stores go past the caches, which the data
+// would fill and nobody read (500 blocks of 24 heads of 128, 397 MB read and written: 58 us, 6.9 TB/s; through
+// them 82 us; loads past them too 76; chunks of 32 KB 117).
 __device__ __forceinline__ void copy_chunk(const PageGeom& g, const PageParts& from, const PageParts& to, int src, int dst,
                                            int chunk) {
   const int of_k = (g.bytes[0] + kChunk - 1) / kChunk, part = chunk >= of_k, at = (chunk - part * of_k) * kChunk;
@@ -63,7 +65,7 @@ __device__ __forceinline__ void copy_chunk(const PageGeom& g, const PageParts& f
     if ((int)(threadIdx.x + 256 * i) * 16 < n) x[i] = a[threadIdx.x + 256 * i];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if ((int)(threadIdx.x + 256 * i) * 16 < n) b[threadIdx.x + 256 * i] = x[i];
+    if ((int)(threadIdx.x + 256 * i) * 16 < n) __builtin_nontemporal_store(x[i], &b[threadIdx.x + 256 * i]);
   if (chunk) return;
 #pragma unroll
   for (int p = 2; p < kPageParts; ++p) {
@@ -92,32 +94,42 @@ struct Entries {
   int* ends;       // [kThreads]: entries up to and with the slot's
   int* firsts;     // [kThreads]: its first entry
 
+  // Takes the slots from s0 on; returns their entries' number.
+  __device__ __forceinline__ int take(int s0) const {
+    const int s = s0 + threadIdx.x;
+    int j0 = 0, n = 0;
+    if (s < g.slots) {
+      const int at = start[s], more = tokens[s];
+      if (at >= 0 && more > 0) {
+        j0 = min(at / RC_KV_BLOCK, g.seq_blocks);
+        n = max(min(blocks_of((int64_t)at + more), g.seq_blocks) - j0, 0);
+      }
+    }
+    int all;
+    const int lead = before(n, sums, all);
+    ends[threadIdx.x] = lead + n;
+    firsts[threadIdx.x] = j0;
+    __syncthreads();
+    return all;
+  }
+  // Slot (from s0 on) and place in its row of entry e of `all`.
+  __device__ __forceinline__ void find(int e, int all, int& slot, int& j) const {
+    int lo = 0;  // the first slot whose entries end after e
+#pragma unroll
+    for (int step = kThreads / 2; step; step /= 2)
+      if (e < all && ends[lo + step - 1] <= e) lo += step;
+    slot = lo;
+    j = e < all ? firsts[lo] + e - (lo ? ends[lo - 1] : 0) : 0;
+  }
   // Calls what(live, slot, j) for every entry, by all threads together.
   template <typename F>
   __device__ __forceinline__ void each(F&& what) const {
     for (int s0 = 0; s0 < g.slots; s0 += kThreads) {
-      const int s = s0 + threadIdx.x;
-      int j0 = 0, n = 0;
-      if (s < g.slots) {
-        const int at = start[s], more = tokens[s];
-        if (at >= 0 && more > 0) {
-          j0 = min(at / RC_KV_BLOCK, g.seq_blocks);
-          n = max(min(blocks_of((int64_t)at + more), g.seq_blocks) - j0, 0);
-        }
-      }
-      int all;
-      const int lead = before(n, sums, all);
-      ends[threadIdx.x] = lead + n;
-      firsts[threadIdx.x] = j0;
-      __syncthreads();
+      const int all = take(s0);
       for (int e0 = 0; e0 < all; e0 += kThreads) {
-        const int e = e0 + threadIdx.x;
-        int lo = 0;  // the first slot whose entries end after e
-#pragma unroll
-        for (int step = kThreads / 2; step; step /= 2)
-          if (e < all && ends[lo + step - 1] <= e) lo += step;
-        const int j = e < all ? firsts[lo] + e - (lo ? ends[lo - 1] : 0) : 0;
-        what(e < all, s0 + lo, j);
+        int s, j;
+        find(e0 + threadIdx.x, all, s, j);
+        what(e0 + (int)threadIdx.x < all, s0 + s, j);
       }
       __syncthreads();
     }
@@ -135,7 +147,75 @@ __global__ __launch_bounds__(kThreads) void pages_reserve_kernel(PageGeom g, Pag
     const int p = live ? table[(int64_t)s * g.seq_blocks + j] : -1;
     return (unsigned)p < (unsigned)g.pool_blocks ? p : -1;
   };
+  // The free ones among four blocks of each thread from block p0 on; returns how many all threads have, and
+  // gives those before the need-th to `to`.
+  const auto find_free = [&](const int (&count)[4], int p0, int found, int need, int* to) {
+    const int p = p0 + 4 * threadIdx.x;
+    int n = 0, all;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n += p + i < g.pool_blocks && count[i] <= 0;
+    int at = found + before(n, sums, all);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (p + i < g.pool_blocks && count[i] <= 0) {
+        if (at < need) to[at] = p + i;
+        ++at;
+      }
+    return all;
+  };
+  const auto counts = [&](int p0, int (&count)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) count[i] = refs[min(p0 + (int)(4 * threadIdx.x) + i, g.pool_blocks - 1)];
+  };
   for (int s = threadIdx.x; s < g.slots; s += kThreads) w.pairs[s] = make_int2(-1, -1);
+  if (g.slots <= kThreads) {
+    // A thread for each entry, if there are as many: what it has read stays in its registers (64 sequences,
+    // five tokens each: 5.1 us, by the passes below 12.7).
+    int count[4];
+    counts(0, count);  // in flight meanwhile
+    const int all = entries.take(0);
+    if (all <= kThreads) {
+      __shared__ int list[kThreads];
+      int s, j;
+      const bool live = (int)threadIdx.x < all;
+      entries.find(threadIdx.x, all, s, j);
+      const int p = block_at(live, s, j), holders = p >= 0 ? refs[p] : 0;
+      const bool shared = holders > 1;
+      bool keeps = false;
+      if (__syncthreads_or(shared)) {
+        if (shared) {
+          atomicAdd(&w.writers[p], 1);
+          atomicMin(&w.first[p], s * g.seq_blocks + j);
+        }
+        __threadfence();
+        __syncthreads();
+        if (shared) keeps = fresh(&w.writers[p]) == holders && fresh(&w.first[p]) == s * g.seq_blocks + j;
+      }
+      const bool mine = live && (p < 0 || (shared && !keeps));
+      int need;
+      const int rank = before(mine, sums, need);
+      int found = 0;
+      for (int p0 = 0; p0 < g.pool_blocks && found < need; p0 += 4 * kThreads) {
+        if (p0) counts(p0, count);
+        found += find_free(count, p0, found, need, list);
+      }
+      if (missing && threadIdx.x == 0) *missing = max(need - found, 0);
+      __syncthreads();
+      if (shared) {
+        w.writers[p] = 0;
+        w.first[p] = INT32_MAX;
+      }
+      if (found >= need && mine) {
+        const int q = list[rank];
+        if (p >= 0 && (int64_t)j * RC_KV_BLOCK < start[s]) w.pairs[s] = make_int2(p, q);
+        table[(int64_t)s * g.seq_blocks + j] = q;
+        refs[q] = 1;
+        if (p >= 0) atomicSub(&refs[p], 1);
+      }
+      return;
+    }
+    __syncthreads();
+  }
   // who would write each shared block
   entries.each([&](bool live, int s, int j) {
     const int p = block_at(live, s, j);
@@ -161,22 +241,9 @@ __global__ __launch_bounds__(kThreads) void pages_reserve_kernel(PageGeom g, Pag
   // the first `need` free blocks
   int found = 0;
   for (int p0 = 0; p0 < g.pool_blocks && found < need; p0 += 4 * kThreads) {
-    const int p = p0 + 4 * threadIdx.x;
-    bool free[4];
-    int n = 0, all;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      free[i] = p + i < g.pool_blocks && refs[p + i] <= 0;
-      n += free[i];
-    }
-    int at = found + before(n, sums, all);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (free[i]) {
-        if (at < need) w.list[at] = p + i;
-        ++at;
-      }
-    found += all;
+    int count[4];
+    counts(p0, count);
+    found += find_free(count, p0, found, need, w.list);
   }
   const bool enough = found >= need;
   if (missing && threadIdx.x == 0) *missing = enough ? 0 : need - found;
@@ -241,6 +308,32 @@ __global__ __launch_bounds__(256) void pages_rows_kernel(PageGeom g, const int32
   const int s = blockIdx.y, j = blockIdx.x * 256 + threadIdx.x;
   if ((unsigned)source[s] >= (unsigned)g.slots || j >= g.seq_blocks) return;
   table[(int64_t)s * g.seq_blocks + j] = rows[(int64_t)s * g.seq_blocks + j];
+}
+
+// Both at once, by one block of threads, for tables of up to kForkEntries entries (2304 entries:
+// 4.0 us, by the two above 4.8 and a launch).
+constexpr int kForkEach = 8, kForkEntries = kForkEach * kThreads;
+__global__ __launch_bounds__(kThreads) void pages_fork_small_kernel(PageGeom g, int32_t* refs, int32_t* table,
+                                                                    const int32_t* source, const int32_t* length) {
+  int now[kForkEach], was[kForkEach];
+#pragma unroll
+  for (int k = 0; k < kForkEach; ++k) {
+    const int i = threadIdx.x + k * kThreads, s = i / g.seq_blocks, j = i % g.seq_blocks;
+    const int from = s < g.slots ? source[s] : -1;
+    was[k] = now[k] = -1;
+    if ((unsigned)from < (unsigned)g.slots) {
+      was[k] = table[i];
+      if (j < blocks_of(max(length[s], 0))) now[k] = table[(int64_t)from * g.seq_blocks + j];
+    }
+  }
+  __syncthreads();  // all rows are read
+#pragma unroll
+  for (int k = 0; k < kForkEach; ++k) {
+    if (was[k] == now[k]) continue;
+    if ((unsigned)was[k] < (unsigned)g.pool_blocks) atomicSub(&refs[was[k]], 1);
+    if ((unsigned)now[k] < (unsigned)g.pool_blocks) atomicAdd(&refs[now[k]], 1);
+    table[threadIdx.x + k * kThreads] = now[k];
+  }
 }
 
 __global__ __launch_bounds__(256) void pages_free_kernel(PageGeom g, int32_t* refs, int32_t* table, const int32_t* keep) {
@@ -341,6 +434,10 @@ hipError_t launch_pages_reserve(const PageGeom& g, const PageWork& w, const Page
 
 hipError_t launch_pages_fork(const PageGeom& g, const PageWork& w, int32_t* refs, int32_t* table, const int32_t* source,
                              const int32_t* length, hipStream_t s) {
+  if ((int64_t)g.slots * g.seq_blocks <= kForkEntries) {
+    pages_fork_small_kernel<<<1, kThreads, 0, s>>>(g, refs, table, source, length);
+    return hipGetLastError();
+  }
   pages_fork_kernel<<<row_grid(g), 256, 0, s>>>(g, w.rows, refs, table, source, length);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;

@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # LIBRESCOMP_LIB names another build of the library (the CPU sanitizer build
@@ -144,8 +145,8 @@ def _load():
     lib.rc_kv_workspace_bytes.argtypes = [vp]
     i = ctypes.c_int
     lib.rc_attn_plan_create.argtypes = [rc_attn_shape_t, i, ctypes.POINTER(rc_attn_params_t), ctypes.POINTER(vp)]
-    lib.rc_attn_packed.argtypes = [vp, vp, i, vp, vp, i, i, i, i, view, view, view, view, vp]
-    lib.rc_attn_join.argtypes = [vp, i, view, ctypes.POINTER(vp), i, i, i, i, view, vp]
+    lib.rc_attn_packed.argtypes = [vp, vp, i, vp, vp, i, i, i, i, vp, vp, vp, vp, vp]  # views: rc_kv_view_t, or its bytes
+    lib.rc_attn_join.argtypes = [vp, i, vp, ctypes.POINTER(vp), i, i, i, i, vp, vp]
     lib.rc_attn_plan_destroy.argtypes = [vp]
     lib.rc_pages_plan_create.argtypes = [rc_pages_shape_t, ctypes.POINTER(vp)]
     lib.rc_pages_reserve.argtypes = [vp, vp, cache, vp, vp, vp, vp, vp]
@@ -671,35 +672,49 @@ def rc_attn_join(stream, outs, lses, batch, tokens, heads, head_dim, out: rc_kv_
            "rc_attn_join")
 
 
-_torch = _codes = None
+_torch = _codes = _int32 = _float32 = None
 
 
 def _need_torch():
     """torch, for the checks of the classes below (importing this module does not need it)."""
-    global _torch, _codes
+    global _torch, _codes, _int32, _float32
     if _torch is None:
         import torch
         _torch, _codes = torch, {torch.bfloat16: RC_BF16, torch.float32: RC_F32}
+        _int32, _float32 = torch.int32, torch.float32
     return _torch
 
 
+def _device():
+    """The current device, whose stream and memory the calls below use; -2 without one."""
+    try:
+        return _torch._C._cuda_getDevice()
+    except Exception:
+        return -2
+
+
 def _on_current(x, what):
-    """Refuses host tensors, and those of another device than the current one, whose stream and
-    memory the call uses."""
-    if not x.is_cuda:
+    """Refuses host tensors, and those of another device than the current one."""
+    device = x.get_device()
+    if device < 0:
         raise ValueError("%s must be a device tensor" % what)
-    if x.get_device() != _torch._C._cuda_getDevice():
-        raise ValueError("%s is on device %d, the current one is %d" % (what, x.get_device(), _torch._C._cuda_getDevice()))
+    if device != _device():
+        raise ValueError("%s is on device %d, the current one is %d" % (what, device, _device()))
 
 
-def _array(x, n, what, dtype="int32"):
-    """Pointer of a contiguous device tensor of n values, None for None."""
+def _array(x, n, what, dtype=None, device=None):
+    """Pointer of a contiguous device tensor of n values (int32, or fp32), None for None."""
     if x is None:
         return None
-    _on_current(x, what)
-    if x.dtype is not getattr(_torch, dtype) or not x.is_contiguous() or x.numel() != n:
-        raise ValueError("%s must be a contiguous %s device tensor of %d values" % (what, dtype, n))
+    if x.get_device() != device:
+        _on_current(x, what)
+    if x.dtype is not (dtype or _int32) or x.numel() != n or not x.is_contiguous():
+        raise ValueError("%s must be a contiguous %s device tensor of %d values" % (what, dtype or _int32, n))
     return x.data_ptr()
+
+
+# An rc_kv_view_t as bytes: data, dtype, strides of batch, token and head (half the time of the structure).
+_view = struct.Struct("Pi4xqqq").pack
 
 
 class AttnPlan:
@@ -712,34 +727,40 @@ class AttnPlan:
         self.handle = None
         self.q_heads, self.kv_heads, self.head_dim = int(q_heads), int(kv_heads), int(head_dim)
         self.dtype = DTYPES.get(dtype, dtype)
+        self._type = {RC_BF16: _torch.bfloat16, RC_F32: _torch.float32}.get(self.dtype)
         self.handle = rc_attn_plan_create((self.q_heads, self.kv_heads, self.head_dim, int(max_seqs), int(max_queries),
                                            int(max_keys)), self.dtype,
                                           rc_attn_params_t(float(scale), RC_ATTN_CAUSAL if causal else 0))
         self.workspace_bytes = rc_attn_workspace_bytes(self.handle)
 
-    def _rows(self, x, tokens, heads, what):
-        _on_current(x, what)
-        if x.dim() != 3 or tuple(x.shape) != (tokens, heads, self.head_dim):
-            raise ValueError("%s is %s, the call takes (%d, %d, %d)" % (what, tuple(x.shape), tokens, heads, self.head_dim))
-        if _codes.get(x.dtype) != self.dtype:
-            raise ValueError("%s is %s, the plan takes %s" % (what, x.dtype, "bfloat16" if self.dtype == RC_BF16 else "float32"))
-        t, h, d = x.stride() if tokens else (heads * self.head_dim, self.head_dim, 1)  # torch's are any where nothing is
+    def _rows(self, x, shape, what, device):
+        if x.get_device() != device:
+            _on_current(x, what)
+        if x.shape != shape:
+            raise ValueError("%s is %s, the call takes %s" % (what, tuple(x.shape), shape))
+        if x.dtype is not self._type:
+            raise ValueError("%s is %s, the plan takes %s" % (what, x.dtype, self._type))
+        t, h, d = x.stride() if shape[0] else (shape[1] * shape[2], shape[2], 1)  # torch's are any where nothing is
         if d != 1:
             raise ValueError("%s must have contiguous rows of head_dim" % what)
-        return rc_kv_view_t(x.data_ptr(), self.dtype, 0, t, h)
+        return _view(x.data_ptr(), self.dtype, 0, t, h)
 
     def attend(self, q, k, v, q_offsets, out, lse=None, kv_offsets=None, max_q=0, max_kv=0, stream=None):
         """Attention of q [query tokens, q_heads, head_dim] over k, v [key tokens, kv_heads,
         head_dim] of the same sequence; q_offsets (and kv_offsets, if the keys' differ): int32
         [sequences + 1]. Writes out, like q, and lse, fp32 [query tokens, q_heads]. max_q, max_kv:
         bounds of one sequence's lengths, if known."""
-        nq, nk = q.shape[0], k.shape[0]
-        views = (self._rows(q, nq, self.q_heads, "q"), self._rows(k, nk, self.kv_heads, "k"),
-                 self._rows(v, nk, self.kv_heads, "v"), self._rows(out, nq, self.q_heads, "out"))
-        seqs = q_offsets.numel() - 1
-        rc_attn_packed(self.handle, stream, seqs, _array(q_offsets, seqs + 1, "q_offsets"),
-                       _array(kv_offsets, seqs + 1, "kv_offsets"), nq, nk, max_q, max_kv, *views,
-                       _array(lse, nq * self.q_heads, "lse", "float32"))
+        nq, nk, seqs = q.shape[0], k.shape[0], q_offsets.numel() - 1
+        rows, keys = (nq, self.q_heads, self.head_dim), (nk, self.kv_heads, self.head_dim)
+        device = _device()
+        views = (self._rows(q, rows, "q", device), self._rows(k, keys, "k", device), self._rows(v, keys, "v", device),
+                 self._rows(out, rows, "out", device))
+        offsets = (_array(q_offsets, seqs + 1, "q_offsets", _int32, device),
+                   _array(kv_offsets, seqs + 1, "kv_offsets", _int32, device))
+        lse = _array(lse, nq * self.q_heads, "lse", _float32, device)
+        status = _lib.rc_attn_packed(self.handle, _stream(stream), seqs, *offsets, nq, nk, max_q, max_kv, *views, lse)
+        if status:
+            _check(status, "rc_attn_packed")
 
     def close(self):
         if self.handle is not None:
@@ -770,19 +791,27 @@ def join_attention(outs, lses, out, lse=None, stream=None):
         raise ValueError("out is %s, with %d outputs and %d log-sum-exps" % (tuple(shape), len(outs), len(lses)))
     if out.numel() == 0:
         return
-    views = []
-    for what, x in [("out", out)] + [("outs[%d]" % i, x) for i, x in enumerate(outs)]:
-        _on_current(x, what)
-        if x.shape != shape or x.dtype not in _codes:
-            raise ValueError("%s is %s %s, the call takes bfloat16 or float32 of %s" % (what, tuple(x.shape), x.dtype, tuple(shape)))
-        stride = x.stride()
-        if stride[-1] != 1:
-            raise ValueError("%s must have contiguous rows of head_dim" % what)
-        views.append(rc_kv_view_t(x.data_ptr(), _codes[x.dtype], stride[0] if len(shape) == 4 else 0, stride[-3], stride[-2]))
-    batch, (tokens, heads, dim) = shape[0] if len(shape) == 4 else 1, shape[-3:]
+    views, device = [], _device()
+    for x in (*outs, out):
+        code = _codes.get(x.dtype)
+        if x.shape != shape or code is None:
+            raise ValueError("%s is %s %s, the call takes bfloat16 or float32 of %s" % (
+                "outs[%d]" % len(views) if len(views) < len(outs) else "out", tuple(x.shape), x.dtype, tuple(shape)))
+        if x.get_device() != device:
+            _on_current(x, "outs[%d]" % len(views) if len(views) < len(outs) else "out")
+        *b, t, h, d = x.stride()
+        if d != 1:
+            raise ValueError("outs and out must have contiguous rows of head_dim")
+        views.append(_view(x.data_ptr(), code, b[0] if b else 0, t, h))
+    *b, tokens, heads, dim = shape
+    batch = b[0] if b else 1
     n = batch * tokens * heads
-    rc_attn_join(stream, views[1:], [_array(x, n, "lses[%d]" % i, "float32") for i, x in enumerate(lses)], batch, tokens,
-                 heads, dim, views[0], _array(lse, n, "lse", "float32"))
+    lses = (ctypes.c_void_p * len(outs))(*[_array(x, n, "lses", _float32, device) for x in lses])
+    lse = _array(lse, n, "lse", _float32, device)
+    status = _lib.rc_attn_join(_stream(stream), len(outs), b"".join(views[:-1]), lses, batch, tokens, heads, dim,
+                               views[-1], lse)
+    if status:
+        _check(status, "rc_attn_join")
 
 
 # ------------------------------------------------------------------ pages of the cache
@@ -844,42 +873,52 @@ class PagePlan:
         return (_torch.zeros(self.pool_blocks, dtype=_torch.int32, device=device),
                 _torch.full((self.slots, self.seq_blocks), -1, dtype=_torch.int32, device=device))
 
-    def _state(self, refs, table):
-        return _array(refs, self.pool_blocks, "refs"), _array(table, self.slots * self.seq_blocks, "table")
+    def _state(self, refs, table, device):
+        return (_array(refs, self.pool_blocks, "refs", _int32, device),
+                _array(table, self.slots * self.seq_blocks, "table", _int32, device))
 
-    def _cache(self, cache):
+    def _slots(self, x, what, device):
+        return _array(x, self.slots, what, _int32, device)
+
+    def _cache(self, cache, device):
         if cache.geometry != self.geometry:
             raise ValueError("the cache has (blocks, heads, head_dim) %s, the plan %s" % (cache.geometry, self.geometry))
-        _on_current(cache.k, "the cache")
+        if cache.k.get_device() != device:
+            _on_current(cache.k, "the cache")
         return cache.struct
 
     def reserve(self, cache, refs, table, start, tokens, missing=None, stream=None):
         """Give every sequence s blocks of its own for tokens[s] new tokens from start[s] on; missing:
         int32 [1], 0 or how many blocks are lacking (then nothing changes)."""
-        rc_pages_reserve(self.handle, stream, self._cache(cache), *self._state(refs, table),
-                         _array(start, self.slots, "start"), _array(tokens, self.slots, "tokens"),
-                         _array(missing, 1, "missing"))
+        device = _device()
+        rc_pages_reserve(self.handle, stream, self._cache(cache, device), *self._state(refs, table, device),
+                         self._slots(start, "start", device), self._slots(tokens, "tokens", device),
+                         _array(missing, 1, "missing", _int32, device))
 
     def fork(self, refs, table, source, length, stream=None):
         """Sequence s continues sequence source[s] (-1: stays) from its first length[s] tokens on."""
-        rc_pages_fork(self.handle, stream, *self._state(refs, table), _array(source, self.slots, "source"),
-                      _array(length, self.slots, "length"))
+        device = _device()
+        rc_pages_fork(self.handle, stream, *self._state(refs, table, device), self._slots(source, "source", device),
+                      self._slots(length, "length", device))
 
     def free(self, refs, table, keep, stream=None):
         """Keep the first keep[s] tokens of every sequence and give the blocks behind them back."""
-        rc_pages_free(self.handle, stream, *self._state(refs, table), _array(keep, self.slots, "keep"))
+        device = _device()
+        rc_pages_free(self.handle, stream, *self._state(refs, table, device), self._slots(keep, "keep", device))
 
     def compact(self, cache, refs, table, used=None, moved=None, stream=None):
         """Move the blocks in use to the front of the pool; used: int32 [1], their number; moved: int32
         [pool_blocks], each block's place now."""
-        rc_pages_compact(self.handle, stream, self._cache(cache), *self._state(refs, table), _array(used, 1, "used"),
-                         _array(moved, self.pool_blocks, "moved"))
+        device = _device()
+        rc_pages_compact(self.handle, stream, self._cache(cache, device), *self._state(refs, table, device),
+                         _array(used, 1, "used", _int32, device), _array(moved, self.pool_blocks, "moved", _int32, device))
 
     def copy(self, cache, src, dst, to=None, stream=None):
         """Copy block src[i] of the cache to block dst[i] of `to` (of the same cache by default)."""
-        source, count = self._cache(cache), src.numel()
-        rc_pages_copy(self.handle, stream, source, source if to is None else self._cache(to), _array(src, count, "src"),
-                      _array(dst, count, "dst"), count)
+        device = _device()
+        source, count = self._cache(cache, device), src.numel()
+        rc_pages_copy(self.handle, stream, source, source if to is None else self._cache(to, device),
+                      _array(src, count, "src", _int32, device), _array(dst, count, "dst", _int32, device), count)
 
     def close(self):
         if self.handle is not None:
