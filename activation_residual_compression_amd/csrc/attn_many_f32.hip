@@ -2,7 +2,7 @@
 //
 // fp32 products on the f16 matrix units, which are 8.5 times as fast as those for fp32 (1196 and 141
 // TFLOP/s measured): x = 2^e (x1 + x2), x1 and x2 in f16 and e the row's own, so that its largest is
-// in [2^14, 2^15): 22 bits of each value down to 2^-17 of it, and 2^-40 of it below. A product is
+// in [2^14, 2^15): 22 bits of each value down to 2^-17 of it, and to 2^-39 of it below. A product is
 // x1 y1 + x1 y2 + x2 y1; x2 y2, under 2^-22 of it, is left out.
 //
 // The split of K and V is done once for all rows that read them, by a kernel before, into the
@@ -12,8 +12,17 @@
 //
 // The attention is that of the kernel for bf16 (S^T = K Q^T, O^T = V^T P^T, tiles past the
 // registers into two LDS buffers), with p = 2^(S 2^(eq + ek) c - m), of which l is the sum, and
-// w = p 2^ev as weights of V's halves: m is raised when the w of a step sum to more than 2^14,
-// so that w fits f16 and is split like the rest.
+// w = p 2^ev as weights of V's halves: m is raised when a w passes 2^15, to where the largest is 2^8,
+// so that w fits f16 and is split like the rest (to 2^-33 of a row's largest).
+//
+// Bound by the matrix units at the clock that the card's power allows (1.6 GHz): 8192 queries over
+// 8192 keys, 16 heads of 128: 1.60 ms, 344 TFLOP/s of attention, 1.03 PFLOP/s of f16 products (a large
+// one of the library: 1.20), the matrix units busy 60 % of the cycles; heads of 64: 0.98 ms, 49 %,
+// where the splitting of the weights (9 vector instructions each) takes as long as the products.
+// Three waves of a SIMD and tiles of 32 keys for D = 64 (4444 over 4444, 30 heads: 556 us, two waves
+// and 64 keys 585); the factors of a step's keys are read before its products (542). The products of
+// one half of a tile beside the weights of the other, as in the bf16 kernel: 559. On the fp32 matrix
+// units, by the kernel for few rows: 1566.
 #include <algorithm>
 
 #include "attn_many.hpp"
@@ -21,7 +30,7 @@
 namespace rc {
 namespace {
 
-constexpr float kMost = 0x1p14f, kAbove = 4.0f;  // log2 of the largest weight after m is raised
+constexpr float kMost = 0x1p15f, kAbove = 8.0f;  // log2 of the largest weight after m is raised
 constexpr int kExp = 14, kLeast = -90;  // exponent of a row's largest value; e is not below kLeast
 constexpr int kBias = 27;               // the factor of a key is 2^(e - kBias), so that it does not take a score out of fp32
 

@@ -75,8 +75,8 @@ rc_status_t rc_attn_plan_create(rc_attn_shape_t shape, rc_dtype_t dtype, const r
  * for their sum: before the last rounding an output is within 2^-8 of the weighted mean of
  * |v|. In fp32 the factors of a product (q, k, v and the weights) may be taken as sums of two
  * f16, 22 bits each, on a scale of their row of head_dim values: of a row's values under 2^-17
- * of its largest, and of weights (times the largest |v| of their token) under 2^-17 of a
- * query's largest, those bits are lost that lie under 2^-40 of it.
+ * of its largest those bits are lost that lie under 2^-39 of it, of weights (times the largest
+ * |v| of their token) those under 2^-33 of a query's largest.
  * NaN and infinities: what a query does not see does not reach it, whatever it holds. A
  * NaN among the queries, or the keys that one sees, or a score of +infinity makes its
  * outputs and lse NaN; a value that is not finite makes the outputs that see it not finite. */

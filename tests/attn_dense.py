@@ -52,7 +52,8 @@ def attend(q, k, v, causal, scale):
             out[:, h] = p @ vv / np.where(none, 1.0, total)[:, None]
             lse[:, h] = np.where(none, -np.inf, m0[:, 0] + np.log(np.where(none, 1.0, total)))
             weight[:, h] = p @ np.abs(vv) / np.where(none, 1.0, total)[:, None]
-            logit[:, h] = np.where(see, np.abs(q[:, h]) @ np.abs(kk).T * scale, 0.0).max(1, initial=0.0)
+            # a score of -infinity has no error (its weight is zero), one of +infinity or NaN makes its row NaN
+            logit[:, h] = np.where(see & np.isfinite(s), np.abs(q[:, h]) @ np.abs(kk).T * scale, 0.0).max(1, initial=0.0)
         strange[:, h] = ((see & some[:, None]).astype(float) @ odd) > 0
     return out, lse, weight, logit, strange
 
