@@ -98,7 +98,7 @@ constexpr Form kForms64[] = {{1, 1, 4, {0.95, 1.27, 1.61, 1.94}, 4.2, 5.1, 0.106
                              {2, 2, 1, {2.01}, 6.7, 6.1, 0.108}};
 
 // fp32, its one form, of 128 and of 64: 16 heads, 4096 keys and 256, 512 (and 768) blocks of threads.
-constexpr Form kFormsF32[] = {{1, 1, 2, {3.57, 6.02}, 6.0, 8.0, 0.12}, {1, 1, 3, {2.48, 3.64, 5.01}, 5.0, 8.0, 0.12}};
+constexpr Form kFormsF32[] = {{1, 1, 2, {3.33, 5.56}, 6.0, 8.0, 0.12}, {1, 1, 3, {2.41, 3.49, 4.68}, 5.0, 8.0, 0.12}};
 
 double cost_of(const rc_attn_plan* pl, const Call& c, const Form& f, int64_t parts) {
   const rc_attn_shape_t& s = pl->shape;
