@@ -51,8 +51,9 @@ __host__ __device__ __forceinline__ int chunks_of(const PageGeom& g) {
   return (g.bytes[0] + kChunk - 1) / kChunk + (g.bytes[1] + kChunk - 1) / kChunk;
 }
 // Copies chunk `chunk` of block src to block dst; 256 threads. The stores go past the caches, which the data
-// would fill and nobody read (500 blocks of 24 heads of 128, 397 MB read and written: 58 us, 6.9 TB/s; through
-// them 82 us; loads past them too 76; chunks of 32 KB 117).
+// would fill and nobody read (500 blocks of 24 heads of 128, 397 MB read and written, the source in the last-level
+// cache: 58 us, 6.9 TB/s, stores through it 82; all from HBM: 80, 83). Loads past it too are faster from HBM (76) and
+// slower from the cache (76).
 __device__ __forceinline__ void copy_chunk(const PageGeom& g, const PageParts& from, const PageParts& to, int src, int dst,
                                            int chunk) {
   const int of_k = (g.bytes[0] + kChunk - 1) / kChunk, part = chunk >= of_k, at = (chunk - part * of_k) * kChunk;
@@ -77,7 +78,9 @@ __device__ __forceinline__ void copy_chunk(const PageGeom& g, const PageParts& f
 
 __global__ __launch_bounds__(256) void pages_copy_kernel(PageGeom g, PageParts from, PageParts to, const int32_t* src,
                                                          const int32_t* dst, int chunks) {
-  const int i = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
+  // Blocks of threads go to the 8 XCDs in turn; each gets a run of the work (77 us, in turn 80).
+  const int runs = gridDim.x / 8, w = (int)blockIdx.x < 8 * runs ? (int)blockIdx.x % 8 * runs + (int)blockIdx.x / 8 : (int)blockIdx.x;
+  const int i = w / chunks, chunk = w % chunks;
   const int p = src[i], q = dst[i];
   if ((unsigned)p >= (unsigned)g.pool_blocks || (unsigned)q >= (unsigned)g.pool_blocks) return;
   copy_chunk(g, from, to, p, q, chunk);

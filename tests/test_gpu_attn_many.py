@@ -260,3 +260,29 @@ def test_fp32_with_and_without_room_for_halves(max_keys):
         p.attend(q, k, v, ints([0, n]), out, lse)
         torch.cuda.synchronize()
     check_all(q[:, :1], k[:, :1], v[:, :1], [0, n], [0, n], True, 128 ** -0.5, out[:, :1], lse[:, :1], "f32")
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 64), ("f32", 128)])
+def test_join_of_more_than_the_caches_hold(dtype, dim):
+    """Against the sum in 64 bits on the GPU; bounds as in test_gpu_attn's join."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(dim)
+    parts, shape = 3, (2, 1500, 1 + (150 << 20) // (3 * 3000 * dim * (2 if dtype == "bf16" else 4)))
+    say("[gpu] join of large parts %s %s" % (dtype, shape))
+    outs = [torch.randn((*shape, dim), generator=g, device=DEV).to(DT[dtype]) for _ in range(parts)]
+    lses = [torch.randn(shape, generator=g, device=DEV) * 4 for _ in range(parts)]
+    lses[1][1, 3:9] = -float("inf")
+    assert sum(x.numel() * x.element_size() for x in outs) > 128 << 20
+    want = torch.softmax(torch.stack(lses).double(), 0)
+    weight = sum(w[..., None] * x.double().abs() for w, x in zip(want, outs))
+    total = sum(w[..., None] * x.double() for w, x in zip(want, outs))
+    out, lse = torch.empty_like(outs[0]), torch.empty(shape, device=DEV)
+    rc.join_attention(outs, lses, out, lse)
+    torch.cuda.synchronize()
+    bound = weight * (2.0 ** -20 + 176 * 2.0 ** -24) + total.abs() * (4 * 2.0 ** -24 if dtype == "f32" else 2.0 ** -8) + 1e-30
+    assert ((out.double() - total).abs() <= bound).all()
+    log = torch.logsumexp(torch.stack(lses).double(), 0)
+    assert ((lse.double() - log).abs() <= 2.0 ** -20 + 176 * 2.0 ** -24 + 4 * 2.0 ** -24 * log.abs()).all()
+    rc.join_attention(outs, lses, outs[0], lses[0])          # in place
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], out) and torch.equal(lses[0], lse)
