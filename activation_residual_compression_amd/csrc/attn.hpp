@@ -21,6 +21,9 @@ struct AttnArgs {
   // one part it writes the outputs; with more, each writes partial results
   // [part][kv_heads * q_tokens * group][D] and (m, l), which are joined.
   int splits, chunk;
+  // How blocks of threads find their rows: 0, from the lengths of all sequences; else every sequence has as
+  // many blocks as the longest may need (the kernel for many rows: this many tiles).
+  int direct;
   float* part;
   float2* part_ml;
   uint32_t* arrived;       // [groups of rows], zero between calls

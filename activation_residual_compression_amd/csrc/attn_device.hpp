@@ -15,6 +15,11 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
   const int k0 = min(max(a.kv_off[b], 0), a.kv_tokens), k1 = min(a.kv_off[b + 1], a.kv_tokens);
   return {q0, min(max(q1 - q0, 0), a.max_q), k0, min(max(k1 - k0, 0), a.max_kv)};
 }
+// Queries of sequence b.
+__device__ __forceinline__ int attn_queries(const AttnArgs& a, int b) {
+  const int q0 = min(max(a.q_off[b], 0), a.q_tokens), q1 = min(a.q_off[b + 1], a.q_tokens);
+  return min(max(q1 - q0, 0), a.max_q);
+}
 // Keys that query i of the sequence sees.
 __device__ __forceinline__ int attn_limit(const AttnArgs& a, const AttnSeq& s, int i) {
   return a.causal ? max(0, s.nk - s.nq + i + 1) : s.nk;

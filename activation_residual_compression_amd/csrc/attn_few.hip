@@ -52,14 +52,14 @@ struct Piece {
 };
 __device__ __forceinline__ Piece piece_of(const AttnArgs& a, int w, int groups, AttnSeq& s) {
   const int lane = threadIdx.x & 63;
-  if (a.splits == 1 || a.seqs == 1) {
+  if (a.seqs == 1 || a.direct) {
     const int b = a.seqs == 1 ? 0 : w / groups, at = a.seqs == 1 ? w : w % groups;
     s = attn_seq(a, b);
     return {b, at / a.splits, at % a.splits, a.splits};
   }
-  // With several parts the pieces are numbered without gaps, sequence by sequence, so that blocks of
-  // threads that have work are spread evenly. Offsets that descend may claim more pieces than there are
-  // blocks of threads: each group then has one part.
+  // With several parts, or bounds far above the lengths, the pieces are numbered without gaps, sequence by
+  // sequence, so that blocks of threads that have work are spread evenly. Offsets that descend may claim more
+  // pieces than there are blocks of threads: each group then has one part.
   const auto count = [&](int b0, int most, int& parts) {  // pieces of the lane's sequence
     s = attn_seq(a, min(b0 + lane, a.seqs - 1));
     parts = min(max((s.nk + a.chunk - 1) / a.chunk, 1), most);
@@ -68,6 +68,7 @@ __device__ __forceinline__ Piece piece_of(const AttnArgs& a, int w, int groups, 
   int most = a.splits, parts, end = 0;
   if (a.seqs > 64) {
     int64_t all = 0;
+#pragma unroll 4
     for (int b0 = 0; b0 < a.seqs; b0 += 64) all += __builtin_amdgcn_readlane(sum_up_to(count(b0, most, parts)), 63);
     if (all > gridDim.x / a.kv_heads) most = 1;
   }

@@ -57,12 +57,6 @@ __device__ __forceinline__ float sum_halves(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// x of the one lane `lane`.
-__device__ __forceinline__ AttnSeq of_lane(const AttnSeq& s, int lane) {
-  const auto of = [&](int x) { return __builtin_amdgcn_readlane(x, lane); };
-  return {of(s.q0), of(s.nq), of(s.k0), of(s.nk)};
-}
-
 // Sum of x over the wave's lanes, the same in all: inside rows of 16 lanes by moves between
 // neighbours, over the rows by scalars.
 __device__ __forceinline__ int wave_total(int x) {
@@ -84,14 +78,14 @@ __device__ __forceinline__ int wave_top(int x) {  // the largest, of numbers tha
 struct Place {
   int b, h, tile;  // b < 0: none
 };
-__device__ __forceinline__ int tiles_of(const AttnArgs& a, const AttnSeq& s, int rows_per) {
-  return (s.nq * a.group + rows_per - 1) / rows_per;
+__device__ __forceinline__ int tiles_of(const AttnArgs& a, int queries, int rows_per) {
+  return (queries * a.group + rows_per - 1) / rows_per;
 }
 __device__ __forceinline__ Place place_of(const AttnArgs& a, uint32_t w, uint32_t grid, int rows_per, AttnSeq& s) {
   const int lane = thread_again() & 63;
   if (a.seqs == 1) {
     s = attn_seq(a, 0);
-    const uint32_t tiles = (uint32_t)tiles_of(a, s, rows_per);
+    const uint32_t tiles = (uint32_t)tiles_of(a, s.nq, rows_per);
     uint32_t t, h;
     if (a.causal) {
       h = w % (uint32_t)a.kv_heads;
@@ -106,17 +100,42 @@ __device__ __forceinline__ Place place_of(const AttnArgs& a, uint32_t w, uint32_
     return {0, (int)h, (int)(a.causal ? tiles - 1 - t : t)};
   }
   const int h = (int)(w % (uint32_t)a.kv_heads), t = (int)(w / (uint32_t)a.kv_heads);
-  // a lane has the sequences lane, 64 + lane, ...: the first one's tiles are kept, others read again
-  s = attn_seq(a, min(lane, a.seqs - 1));
-  const int mine = lane < a.seqs ? tiles_of(a, s, rows_per) : 0;
+  if (a.direct) {
+    const int tile = a.direct - 1 - t / a.seqs, b = t % a.seqs;
+    s = attn_seq(a, b);
+    return {tile >= 0 && tile < tiles_of(a, s.nq, rows_per) ? b : -1, h, tile};
+  }
+  // A lane has the sequences lane, 64 + lane, ...; tiles of the first EACH of them stay in registers, those of
+  // others are worked out again (a block of threads among 1001 sequences takes 3 us to find its rows).
+  constexpr int EACH = 16;
+  int mine[EACH] = {};
+#pragma unroll
+  for (int i0 = 0; i0 < EACH; i0 += 4) {
+    if (64 * i0 >= a.seqs) break;
+    int n[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n[i] = attn_queries(a, min(64 * (i0 + i) + lane, a.seqs - 1));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine[i0 + i] = 64 * (i0 + i) + lane < a.seqs ? tiles_of(a, n[i], rows_per) : 0;
+  }
   const auto sum_over = [&](int level) {  // tiles at levels from `level` on
-    int n = max(mine - level, 0);
-    for (int b = lane + 64; b < a.seqs; b += 64) n += max(tiles_of(a, attn_seq(a, b), rows_per) - level, 0);
+    int n = 0;
+#pragma unroll
+    for (int i0 = 0; i0 < EACH; i0 += 4) {
+      if (64 * i0 >= a.seqs) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n += max(mine[i0 + i] - level, 0);
+    }
+#pragma unroll 4
+    for (int b = lane + 64 * EACH; b < a.seqs; b += 64) n += max(tiles_of(a, attn_queries(a, b), rows_per) - level, 0);
     return wave_total(n);
   };
   if (sum_over(0) <= t) return {-1, 0, 0};
-  int top = mine;
-  for (int b = lane + 64; b < a.seqs; b += 64) top = max(top, tiles_of(a, attn_seq(a, b), rows_per));
+  int top = 0;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) top = max(top, mine[i]);
+#pragma unroll 4
+  for (int b = lane + 64 * EACH; b < a.seqs; b += 64) top = max(top, tiles_of(a, attn_queries(a, b), rows_per));
   // the level that holds the t-th tile from the top: from lo on there are more than t, from hi on not
   int lo = 0, hi = wave_top(top), above = 0;  // above: tiles at levels from hi on
   while (hi - lo > 1) {
@@ -124,20 +143,25 @@ __device__ __forceinline__ Place place_of(const AttnArgs& a, uint32_t w, uint32_
     if (n > t) lo = mid;
     else hi = mid, above = n;
   }
-  int rank = t - above;  // among the sequences that reach level lo
-  for (int b0 = 0; b0 < a.seqs; b0 += 64) {
-    const AttnSeq own = b0 ? attn_seq(a, min(b0 + lane, a.seqs - 1)) : s;
-    uint64_t reach = __ballot(b0 + lane < a.seqs && tiles_of(a, own, rows_per) > lo);
+  int rank = t - above, b = -1;  // among the sequences that reach level lo
+  const auto take = [&](int b0, int tiles) {
+    if (b >= 0) return;
+    uint64_t reach = __ballot(tiles > lo);
     const int n = __builtin_popcountll(reach);
     if (rank < n) {
       for (; rank; --rank) reach &= reach - 1;
-      const int who = (int)__builtin_ctzll(reach);
-      s = of_lane(own, who);
-      return {b0 + who, h, lo};
+      b = b0 + (int)__builtin_ctzll(reach);
+    } else {
+      rank -= n;
     }
-    rank -= n;
-  }
-  return {-1, 0, 0};
+  };
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) take(64 * i, mine[i]);
+  for (int b0 = 64 * EACH; b0 < a.seqs && b < 0; b0 += 64)
+    take(b0, b0 + lane < a.seqs ? tiles_of(a, attn_queries(a, b0 + lane), rows_per) : 0);
+  if (b < 0) return {-1, 0, 0};
+  s = attn_seq(a, b);
+  return {b, h, lo};
 }
 
 // Four keys of a lane's channel, from four rows of V in LDS.

@@ -40,6 +40,7 @@ struct Way {
   int64_t grid;
   int splits, chunk;
   int64_t part_rows;  // rows of partial results; 0 with one part
+  int direct;
 };
 
 size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
@@ -53,7 +54,12 @@ Way few_way(const rc_attn_plan* pl, const Call& c, int64_t most_rows) {
   const rc_attn_shape_t& s = pl->shape;
   const int64_t rows = c.q_tokens * s.q_heads, groups = ceil_div(c.max_q * c.group, 16), base = c.seqs * s.kv_heads * groups;
   const int64_t at_once = 512;  // blocks of threads that the CUs hold
-  Way w{true, 4, 0, c.seqs * groups, 1, (int)std::max<int64_t>(c.max_kv, 1), 0};
+  Way w{true, 4, 0, c.seqs * groups, 1, (int)std::max<int64_t>(c.max_kv, 1), 0, 1};
+  const int64_t dense = c.q_tokens * c.group / 16 + c.seqs;  // pieces that there can be
+  if (2 * dense < w.grid) {
+    w.grid = dense;
+    w.direct = 0;
+  }
   // Few short sequences: twice as many waves and no parts (333 tokens, 24 heads of 128: 8.1 us, two parts 10.3;
   // 600 tokens, 32 heads on 8: 10.2, three parts 8.5).
   if (base <= 256 && c.max_kv <= 512) {
@@ -70,6 +76,7 @@ Way few_way(const rc_attn_plan* pl, const Call& c, int64_t most_rows) {
   w.chunk = (int)std::max(chunk, ceil_div(ceil_div(c.max_kv, splits), 64) * 64);
   w.part_rows = splits * rows;
   w.grid = groups * std::min(c.seqs * splits, c.kv_tokens / w.chunk + c.seqs);
+  w.direct = 0;
   return w;
 }
 
@@ -140,14 +147,19 @@ Way many_way(const rc_attn_plan* pl, const Call& c, int64_t most_rows) {
   for (int i = 0; i < (f32 ? 1 : 4); ++i) {
     const Form& f = forms[i];
     const int64_t per = 128 * f.u;  // as many tiles of rows as there can be: a sequence ends inside of one
-    const int64_t tiles = std::min(c.q_tokens * c.group / per + c.seqs, c.seqs * ceil_div(c.max_q * c.group, per)) * s.kv_heads;
+    const int64_t most = ceil_div(c.max_q * c.group, per), dense = std::min(c.q_tokens * c.group / per + c.seqs, c.seqs * most);
+    // Among more sequences than a wave has lanes a block's rows are found by going through all of them: not where at
+    // most every second block would have none (1000 sequences of 100, 32 / 8 heads of 128: 505 us,
+    // by their lengths 635; 8000 of 100: 3.5 and 11.3 ms).
+    const int direct = c.seqs > 64 && c.seqs * most <= 2 * dense ? (int)most : 0;
+    const int64_t tiles = (direct ? c.seqs * most : dense) * s.kv_heads;
     for (const int64_t parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
       if (parts > 1 && (parts * 4 > ceil_div(c.max_kv, 64) || tiles * parts * per > most_rows)) break;
       const double us = cost_of(pl, c, f, parts);
       if (least > 0.0 && us >= least) continue;
       least = us;
       best = {false, f.u, f.kg, tiles * parts, (int)parts, (int)std::max<int64_t>(ceil_div(ceil_div(c.max_kv, 64), parts), 1),
-              parts > 1 ? tiles * parts * per : 0};
+              parts > 1 ? tiles * parts * per : 0, direct};
     }
   }
   return best;
@@ -290,6 +302,7 @@ rc_status_t rc_attn_packed(rc_attn_plan_t pl, hipStream_t stream, int seqs, cons
   a.scale = fminf((pl->params.scale > 0.0f ? pl->params.scale : 1.0f / sqrtf((float)s.head_dim)) * kLog2e, FLT_MAX);
   const Way w = way_of(pl, {seqs, q_tokens, kv_tokens, a.max_q, a.max_kv, a.group}, pl->part_rows);
   a.splits = w.splits;
+  a.direct = w.direct;
   a.chunk = w.chunk;
   a.part = static_cast<float*>(pl->ws);
   a.part_ml = reinterpret_cast<float2*>(a.part + w.part_rows * s.head_dim);

@@ -727,6 +727,7 @@ class AttnPlan:
         self.handle = None
         self.q_heads, self.kv_heads, self.head_dim = int(q_heads), int(kv_heads), int(head_dim)
         self.dtype = DTYPES.get(dtype, dtype)
+        self.device = _device()  # where its workspace is
         self._type = {RC_BF16: _torch.bfloat16, RC_F32: _torch.float32}.get(self.dtype)
         self.handle = rc_attn_plan_create((self.q_heads, self.kv_heads, self.head_dim, int(max_seqs), int(max_queries),
                                            int(max_keys)), self.dtype,
@@ -758,7 +759,10 @@ class AttnPlan:
         offsets = (_array(q_offsets, seqs + 1, "q_offsets", _int32, device),
                    _array(kv_offsets, seqs + 1, "kv_offsets", _int32, device))
         lse = _array(lse, nq * self.q_heads, "lse", _float32, device)
-        status = _lib.rc_attn_packed(self.handle, _stream(stream), seqs, *offsets, nq, nk, max_q, max_kv, *views, lse)
+        if device != self.device:
+            raise ValueError("the plan was made on device %d, the current one is %d" % (self.device, device))
+        status = _lib.rc_attn_packed(self.handle, _stream(stream), seqs, *offsets, nq, nk, int(max_q), int(max_kv), *views,
+                                     lse)
         if status:
             _check(status, "rc_attn_packed")
 
@@ -865,6 +869,7 @@ class PagePlan:
         self.handle = None
         self.slots, self.pool_blocks, self.seq_blocks = int(slots), int(pool_blocks), int(seq_blocks)
         self.geometry = (self.pool_blocks, int(kv_heads), int(head_dim))
+        self.device = _device()
         self.handle = rc_pages_plan_create((self.slots, int(kv_heads), int(head_dim), self.pool_blocks, self.seq_blocks))
         self.workspace_bytes = rc_pages_workspace_bytes(self.handle)
 
@@ -874,6 +879,8 @@ class PagePlan:
                 _torch.full((self.slots, self.seq_blocks), -1, dtype=_torch.int32, device=device))
 
     def _state(self, refs, table, device):
+        if device != self.device:
+            raise ValueError("the plan was made on device %d, the current one is %d" % (self.device, device))
         return (_array(refs, self.pool_blocks, "refs", _int32, device),
                 _array(table, self.slots * self.seq_blocks, "table", _int32, device))
 

@@ -286,3 +286,23 @@ def test_join_of_more_than_the_caches_hold(dtype, dim):
     rc.join_attention(outs, lses, outs[0], lses[0])          # in place
     torch.cuda.synchronize()
     assert torch.equal(outs[0], out) and torch.equal(lses[0], lse)
+
+
+@DTYPES
+@pytest.mark.parametrize("qh,kh,dim,lq,bounds", [
+    (4, 4, 128, [100 + 7 * i % 31 for i in range(200)], True),        # as many blocks for each sequence
+    (4, 4, 128, [100 + 7 * i % 31 for i in range(200)], False),
+    (2, 1, 128, [i % 41 for i in range(1100)] + [900], True),         # more sequences than a wave's registers hold
+    (4, 2, 64, [1] * 70, False), (4, 2, 64, [1, 0, 2] * 50, False),   # few rows, far fewer than the bounds
+])
+def test_many_sequences(dtype, qh, kh, dim, lq, bounds):
+    rng = np.random.default_rng(len(lq))
+    lk = [n + i % 5 for i, n in enumerate(lq)]
+    say("[gpu] %d sequences %s bounds %s" % (len(lq), dtype, bounds))
+    q, k, v = (rows(rng, sum(n), h, dim, dtype) for n, h in ((lq, qh), (lk, kh), (lk, kh)))
+    qo, ko = offsets(lq), offsets(lk)
+    out, lse = torch.full_like(q, float("nan")), torch.full((q.shape[0], qh), float("nan"), device=DEV)
+    with rc.AttnPlan(qh, kh, dim, dtype, max_seqs=len(lq), max_queries=q.shape[0], max_keys=k.shape[0], causal=True) as p:
+        p.attend(q, k, v, ints(qo), out, lse, kv_offsets=ints(ko), **(dict(max_q=max(lq), max_kv=max(lk)) if bounds else {}))
+        torch.cuda.synchronize()
+    check_all(q, k, v, qo, ko, True, dim ** -0.5, out, lse, dtype)
