@@ -118,7 +118,7 @@ def test_samples_that_go_on_writing_are_as_if_alone():
     kv0 = [torch.from_numpy(rng.standard_normal((1, prompt, heads, dim))).to(DEV, torch.bfloat16) for _ in range(2)]
     tokens = [[torch.from_numpy(rng.standard_normal((2, 1, heads, dim))).to(DEV, torch.bfloat16) for _ in range(3)] for _ in range(steps)]
 
-    def serve(shared):
+    def serve(shared, captured=False):
         cache = rc.KvCache.empty(pool, heads, dim, DEV)
         pages = rc.PagePlan(2, heads, dim, pool, width)
         refs, table = pages.empty(DEV)
@@ -129,7 +129,25 @@ def test_samples_that_go_on_writing_are_as_if_alone():
                      count=ints([prompt, 0 if shared else prompt]))
             if shared:
                 pages.fork(refs, table, ints([-1, 0]), ints([0, prompt]))
-            for t, (q, k, v) in enumerate(tokens):
+            if captured:      # one step as a graph, whose position moves on by itself
+                at, one = ints([prompt, prompt]), ints([1, 1])
+                q, k, v = (torch.empty_like(x) for x in tokens[0])
+                out, after = torch.empty_like(q), torch.empty_like(at)
+                torch.cuda.synchronize()
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    pages.reserve(cache, refs, table, at, one)
+                    kv.store(cache, at, k, v, table=table)
+                    torch.add(at, 1, out=after)
+                    kv.attend(cache, after, q, out, table=table)
+                    at.copy_(after)
+                for x in tokens:
+                    for to, y in zip((q, k, v), x):
+                        to.copy_(y)
+                    graph.replay()
+                    outs.append(out.clone())
+                    torch.cuda.synchronize()
+            for t, (q, k, v) in enumerate(() if captured else tokens):
                 at = ints([prompt + t] * 2)
                 pages.reserve(cache, refs, table, at, ints([1, 1]))
                 kv.store(cache, at, k, v, table=table)
@@ -142,5 +160,8 @@ def test_samples_that_go_on_writing_are_as_if_alone():
     say("[gpu] two samples of a prompt")
     alone, blocks = serve(False)
     together, fewer = serve(True)
-    assert all(torch.equal(x, y) for x, y in zip(alone, together))
+    assert len(together) == steps and all(torch.equal(x, y) for x, y in zip(alone, together))
     assert blocks == 6 and fewer == 5
+    replayed, fewer = serve(True, captured=True)
+    assert len(replayed) == steps and all(torch.equal(x, y) for x, y in zip(alone, replayed))
+    assert fewer == 5
