@@ -3,6 +3,7 @@ of arguments (nothing is launched), and the dense reference's own masks."""
 import ctypes
 import os
 import re
+import subprocess
 
 import numpy as np
 import pytest
@@ -41,6 +42,14 @@ def test_exports_every_declared_function(rc):
     for n in names:
         assert hasattr(lib, n), n
     assert re.search(r"#define RC_ATTN_MAX_PARTS (\d+)", text).group(1) == str(rc.RC_ATTN_MAX_PARTS)
+
+
+@pytest.mark.parametrize("header", ["librescomp_attn.h", "librescomp_pages.h"])
+def test_headers_are_c(header, tmp_path):
+    src = tmp_path / "x.c"
+    src.write_text('#include "%s"\nint main(void) { return 0; }\n' % header)
+    subprocess.run(["gcc", "-std=c99", "-fsyntax-only", "-Wall", "-Werror", "-D__HIP_PLATFORM_AMD__",
+                    "-I", os.path.join(ROOT, "include"), "-I", "/opt/rocm/include", str(src)], check=True)
 
 
 @pytest.mark.parametrize("bad,want", [
