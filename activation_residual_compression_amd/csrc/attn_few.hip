@@ -13,6 +13,11 @@
 // two bf16 each (16 bits), which costs 16 matrix instructions of 16 cycles a step; in fp32
 // both products are in fp32.
 //
+// Bound by HBM for long keys (one token of 64 sequences of 4000, 32 heads of 128 on 8: 181 us, 5.8
+// TB/s; of 65536 tokens 50 us, 5.3 TB/s, in fp32 99; 8 ragged ones of up to 32768 82 us, 4.7), by the
+// chain of reads for short ones (333 tokens, 24 heads: 8.1 us; 2048 tokens, 32 heads on 8: 9.4).
+// Blocks of threads of one piece and all key heads follow each other: their rows lie next to each
+// other in memory (65536 tokens with the pieces of a head after each other: 54 us).
 #include <type_traits>
 
 #include "attn_device.hpp"
@@ -93,7 +98,8 @@ __device__ __forceinline__ Piece piece_of(const AttnArgs& a, int w, int groups, 
   return {-1, 0, 0, 0};
 }
 
-// The number of a row's parts that a thread joins at a time: their loads are in flight together.
+// The number of a row's parts that a thread joins at a time: their loads are in flight together (2048 tokens: 9.4 us;
+// 8 at a time 9.9, 16 11.0).
 constexpr int kJoin = 4;
 
 template <int D, bool F32, int WAVES>

@@ -898,20 +898,29 @@ class PagePlan:
         """Give every sequence s blocks of its own for tokens[s] new tokens from start[s] on; missing:
         int32 [1], 0 or how many blocks are lacking (then nothing changes)."""
         device = _device()
-        rc_pages_reserve(self.handle, stream, self._cache(cache, device), *self._state(refs, table, device),
-                         self._slots(start, "start", device), self._slots(tokens, "tokens", device),
-                         _array(missing, 1, "missing", _int32, device))
+        cache, state = ctypes.byref(self._cache(cache, device)), self._state(refs, table, device)
+        at, n = self._slots(start, "start", device), self._slots(tokens, "tokens", device)
+        missing = _array(missing, 1, "missing", _int32, device)
+        status = _lib.rc_pages_reserve(self.handle, _stream(stream), cache, *state, at, n, missing)
+        if status:
+            _check(status, "rc_pages_reserve")
 
     def fork(self, refs, table, source, length, stream=None):
         """Sequence s continues sequence source[s] (-1: stays) from its first length[s] tokens on."""
         device = _device()
-        rc_pages_fork(self.handle, stream, *self._state(refs, table, device), self._slots(source, "source", device),
-                      self._slots(length, "length", device))
+        state = self._state(refs, table, device)
+        source, length = self._slots(source, "source", device), self._slots(length, "length", device)
+        status = _lib.rc_pages_fork(self.handle, _stream(stream), *state, source, length)
+        if status:
+            _check(status, "rc_pages_fork")
 
     def free(self, refs, table, keep, stream=None):
         """Keep the first keep[s] tokens of every sequence and give the blocks behind them back."""
         device = _device()
-        rc_pages_free(self.handle, stream, *self._state(refs, table, device), self._slots(keep, "keep", device))
+        state, keep = self._state(refs, table, device), self._slots(keep, "keep", device)
+        status = _lib.rc_pages_free(self.handle, _stream(stream), *state, keep)
+        if status:
+            _check(status, "rc_pages_free")
 
     def compact(self, cache, refs, table, used=None, moved=None, stream=None):
         """Move the blocks in use to the front of the pool; used: int32 [1], their number; moved: int32
