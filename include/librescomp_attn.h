@@ -50,10 +50,12 @@ typedef struct {
 } rc_attn_params_t;
 
 /* Validate the request and allocate the workspace (rc_attn_workspace_bytes) on the
- * current device. dtype: of all tensors of the plan's calls. Errors: RC_ERR_INVALID_ARG
- * (null pointer, bad value), RC_ERR_UNSUPPORTED (a valid value that this library does
- * not implement: another head_dim, more than 65535 sequences or 32767 key heads),
- * RC_ERR_HIP. */
+ * current device: partial results of at most half a gigabyte, and in fp32, for calls of
+ * many rows, max_keys keys and values as halves (if that is at most 4 GB; plans for more
+ * keys run a slower kernel). dtype: of all tensors of the plan's calls. Errors:
+ * RC_ERR_INVALID_ARG (null pointer, bad value), RC_ERR_UNSUPPORTED (a valid value that this
+ * library does not implement: another head_dim, more than 65535 sequences, 32767 key heads
+ * or 2^30 keys, 2^30 query rows, max_queries * q_heads, or more), RC_ERR_HIP. */
 rc_status_t rc_attn_plan_create(rc_attn_shape_t shape, rc_dtype_t dtype, const rc_attn_params_t* params,
                                 rc_attn_plan_t* out);
 

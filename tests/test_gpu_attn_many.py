@@ -306,3 +306,17 @@ def test_many_sequences(dtype, qh, kh, dim, lq, bounds):
         p.attend(q, k, v, ints(qo), out, lse, kv_offsets=ints(ko), **(dict(max_q=max(lq), max_kv=max(lk)) if bounds else {}))
         torch.cuda.synchronize()
     check_all(q, k, v, qo, ko, True, dim ** -0.5, out, lse, dtype)
+
+
+@DTYPES
+@pytest.mark.parametrize("causal", [False, True])
+def test_single_tokens_of_many_ragged_sequences(dtype, causal):
+    """Few rows in parts, numbered over more than 64 sequences."""
+    rng = np.random.default_rng(70)
+    say("[gpu] 70 ragged sequences of one token %s" % dtype)
+    lk = [1 + i * 977 % 6000 for i in range(70)]
+    lk[3], lk[69] = 0, 6001
+    q, k, v = rows(rng, 70, 6, 64, dtype), rows(rng, sum(lk), 2, 64, dtype), rows(rng, sum(lk), 2, 64, dtype)
+    out, lse = run(q, k, v, [1] * 70, lk, causal, dtype)
+    again, sums = run(q, k, v, [1] * 70, lk, causal, dtype)
+    assert torch.equal(out, again) and torch.equal(lse, sums)
