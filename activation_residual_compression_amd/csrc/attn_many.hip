@@ -17,11 +17,11 @@
 // accumulators are rescaled a few times in all, and no maximum is taken otherwise. bf16 and
 // fp32 hold such weights as well as those up to 1; both cancel in out = O / l.
 //
-// Bound by the matrix units and the power they may draw: a tile of 64 keys of a wave with 64 rows
-// is 64 (D 128) matrix instructions of 32 cycles, 2048 of the about 2900 cycles that two such waves
-// of a SIMD take for one of theirs each; the exponentials (8 cycles each, 512) and the LDS reads
-// run beside them. 8192 queries over 8192 keys, 32 heads of 128 on 8: 896 us, 1227 TFLOP/s (a
-// large matrix product of the library: 1251, at the 1.8 GHz that the card's power allows both);
+// Bound by the matrix units and the power they may draw: a tile of 64 keys of a wave with 64 rows is
+// 64 (D 128) matrix instructions of 32 cycles, beside which run 64 weights a lane (a multiply-add, an
+// exponential, an addition, half a conversion each) and the LDS reads. 8192 queries over 8192 keys, 32
+// heads of 128 on 8: 896 us, 1227 TFLOP/s (a large matrix product of the library: 1251), the matrix units
+// 62 % busy at the 1.7 GHz that the card's power allows; at 64 channels 50 %, the vector units 72 %:
 // 4444 over 17776, 30 heads of 64: 650 us, 933 TFLOP/s. U = 2 reads K and V from LDS once for 64
 // rows: with one row group a wave LDS bounds it (1087 us). KG = 2 is for calls of few tiles of
 // rows, where a CU would hold one block of four waves: 1152 over 4608, 2 x 24 heads of 128, 126
@@ -35,7 +35,6 @@ namespace rc {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 constexpr float kMost = 0x1p10f;
 
 template <int D, int U, int KG>

@@ -25,14 +25,14 @@ __device__ __forceinline__ int v_turn(int row) { return D == 128 ? (row & 3) << 
 // makes every later read of LDS wait for it; here the wait is the caller's (vmcnt), once a tile.
 // Nothing else in these kernels uses m0.
 __device__ __forceinline__ void load_lds(uint32_t to, uint32_t offset, const void* base) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds(uint32_t to, const void* at) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(at) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(at) : "memory", "m0");
 }
 
 __device__ __forceinline__ void load_lds_4(uint32_t to, const void* at) {  // 4 bytes a lane
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(at) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(at) : "memory", "m0");
 }
 
 // vmcnt(0). In the form that the compiler understands: it would else go on waiting, tile after
