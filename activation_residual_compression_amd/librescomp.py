@@ -693,6 +693,12 @@ def _device():
         return -2
 
 
+def _plan_device():
+    """The device that a plan's workspace comes to lie on. Does not start torch's side of the GPU, whose
+    current device is the first one before that."""
+    return _device() if _torch.cuda.is_initialized() else 0
+
+
 def _on_current(x, what):
     """Refuses host tensors, and those of another device than the current one."""
     device = x.get_device()
@@ -727,7 +733,7 @@ class AttnPlan:
         self.handle = None
         self.q_heads, self.kv_heads, self.head_dim = int(q_heads), int(kv_heads), int(head_dim)
         self.dtype = DTYPES.get(dtype, dtype)
-        self.device = _device()  # where its workspace is
+        self.device = _plan_device()  # where its workspace is
         self._type = {RC_BF16: _torch.bfloat16, RC_F32: _torch.float32}.get(self.dtype)
         self.handle = rc_attn_plan_create((self.q_heads, self.kv_heads, self.head_dim, int(max_seqs), int(max_queries),
                                            int(max_keys)), self.dtype,
@@ -869,7 +875,7 @@ class PagePlan:
         self.handle = None
         self.slots, self.pool_blocks, self.seq_blocks = int(slots), int(pool_blocks), int(seq_blocks)
         self.geometry = (self.pool_blocks, int(kv_heads), int(head_dim))
-        self.device = _device()
+        self.device = _plan_device()
         self.handle = rc_pages_plan_create((self.slots, int(kv_heads), int(head_dim), self.pool_blocks, self.seq_blocks))
         self.workspace_bytes = rc_pages_workspace_bytes(self.handle)
 
@@ -879,10 +885,11 @@ class PagePlan:
                 _torch.full((self.slots, self.seq_blocks), -1, dtype=_torch.int32, device=device))
 
     def _state(self, refs, table, device):
+        state = (_array(refs, self.pool_blocks, "refs", _int32, device),
+                 _array(table, self.slots * self.seq_blocks, "table", _int32, device))
         if device != self.device:
             raise ValueError("the plan was made on device %d, the current one is %d" % (self.device, device))
-        return (_array(refs, self.pool_blocks, "refs", _int32, device),
-                _array(table, self.slots * self.seq_blocks, "table", _int32, device))
+        return state
 
     def _slots(self, x, what, device):
         return _array(x, self.slots, what, _int32, device)
