@@ -15,7 +15,7 @@ struct rc_attn_plan {
   rc_attn_shape_t shape;
   rc_dtype_t dtype;
   rc_attn_params_t params;
-  void* ws = nullptr;  // partial results: outputs, (m, l); then the counters
+  void* ws = nullptr;  // partial results: outputs, (m, l), which tile they are of; the counters; K and V as halves
   size_t ws_bytes = 0;
   int64_t part_rows = 0;        // rows of partial results that it holds
   uint32_t* arrived = nullptr;  // [kFewGroups], for the kernel for few rows
