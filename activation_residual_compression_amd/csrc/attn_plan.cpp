@@ -70,12 +70,14 @@ Way few_way(const rc_attn_plan* pl, const Call& c, int64_t most_rows) {
   // equal parts of all keys that are read, one for each block of threads; each group's last part is half of one on average
   const int64_t read = c.kv_tokens * s.kv_heads * groups;
   const int64_t chunk = std::max<int64_t>(256, ceil_div(ceil_div(read, std::max(at_once - base / 2, at_once / 2)), 64) * 64);
-  const int64_t splits = std::min({ceil_div(c.max_kv, chunk), most_rows / rows, (int64_t)256});
-  if (splits <= 1) return w;
-  w.splits = (int)splits;
-  w.chunk = (int)std::max(chunk, ceil_div(ceil_div(c.max_kv, splits), 64) * 64);
-  w.part_rows = splits * rows;
-  w.grid = groups * std::min(c.seqs * splits, c.kv_tokens / w.chunk + c.seqs);
+  const int64_t most = std::min({ceil_div(c.max_kv, chunk), most_rows / rows, (int64_t)256});
+  if (most <= 1) return w;
+  // Parts begin at multiples of 64 keys: where the workspace limits them, rounding their length up can leave fewer.
+  w.chunk = (int)std::max(chunk, ceil_div(ceil_div(c.max_kv, most), 64) * 64);
+  w.splits = (int)ceil_div(c.max_kv, w.chunk);
+  w.part_rows = w.splits * rows;
+  // One sequence: piece w is part w % splits of group w / splits. Several are numbered without gaps.
+  w.grid = groups * (c.seqs == 1 ? w.splits : std::min(c.seqs * w.splits, c.kv_tokens / w.chunk + c.seqs));
   w.direct = 0;
   return w;
 }
