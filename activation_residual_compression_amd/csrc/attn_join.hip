@@ -19,12 +19,12 @@ __device__ __forceinline__ T load_16(const void* p) {
 // Values of a lane: 4, or 8 where inputs are bf16. FAR: the data is more than the caches hold, and passes them
 // (29.2 us for the call above, through them 33.9; the same tensors again and again 28.2 and 25.5).
 template <int D, bool IN16, bool OUT16, bool FAR>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnJoinArgs a) {
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnJoinArgs a, int64_t first) {
   constexpr int E = IN16 ? 8 : 4, LANES = D / E;
   constexpr float kLog2e = 1.44269504088896340736f;
   // Blocks of threads go to the 8 XCDs in turn; each gets a run of the rows.
   const uint32_t runs = gridDim.x / 8, w = blockIdx.x < 8 * runs ? blockIdx.x % 8 * runs + blockIdx.x / 8 : blockIdx.x;
-  const int64_t row = (int64_t)w * (256 / LANES) + threadIdx.x / LANES;
+  const int64_t row = (first + w) * (256 / LANES) + threadIdx.x / LANES;
   const int d0 = threadIdx.x % LANES * E;
   if (row >= a.rows) return;
   int h, t;
@@ -98,10 +98,11 @@ template <int D, bool IN16, bool OUT16>
 hipError_t run(const AttnJoinArgs& a, hipStream_t s) {
   constexpr int64_t per = 256 / (D / (IN16 ? 8 : 4));
   const int64_t grid = (a.rows + per - 1) / per;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
-  if (a.rows * a.parts * D * (IN16 ? 2 : 4) > (int64_t)128 << 20) attn_join_kernel<D, IN16, OUT16, true><<<(unsigned)grid, 256, 0, s>>>(a);
-  else attn_join_kernel<D, IN16, OUT16, false><<<(unsigned)grid, 256, 0, s>>>(a);
-  return hipGetLastError();
+  const bool far = a.rows * a.parts * D * (IN16 ? 2 : 4) > (int64_t)128 << 20;
+  return launch_all(grid, [&](int64_t first, unsigned blocks) {
+    if (far) attn_join_kernel<D, IN16, OUT16, true><<<blocks, 256, 0, s>>>(a, first);
+    else attn_join_kernel<D, IN16, OUT16, false><<<blocks, 256, 0, s>>>(a, first);
+  });
 }
 
 template <int D>

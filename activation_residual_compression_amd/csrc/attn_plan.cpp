@@ -214,6 +214,15 @@ int64_t part_rows_at_most(const rc_attn_plan* pl) {
   }
 }
 
+// Threads of the call's largest launch: of the kernel, of the join of its parts, of the split of K and V before it.
+int64_t most_threads(const rc_attn_plan* pl, const Call& c, const Way& w) {
+  const rc_attn_shape_t& s = pl->shape;
+  if (w.few) return w.grid * s.kv_heads * 64 * w.u;
+  const int64_t join = w.splits > 1 ? w.grid / w.splits * (w.u * s.head_dim / 32) * 256 : 0;
+  const int64_t halves = pl->dtype == RC_F32 ? (c.kv_tokens * s.kv_heads * (s.head_dim / 8) + 255) / 256 * 256 : 0;
+  return std::max({w.grid * 256 * w.kg, join, halves});
+}
+
 rc_status_t check(const rc_attn_shape_t& s, rc_dtype_t dtype, const rc_attn_params_t* p) {
   if (!p) return RC_ERR_INVALID_ARG;
   if (s.q_heads < 1 || s.kv_heads < 1 || s.head_dim < 1 || s.max_seqs < 1 || s.max_queries < 1 || s.max_keys < 1)
@@ -302,7 +311,9 @@ rc_status_t rc_attn_packed(rc_attn_plan_t pl, hipStream_t stream, int seqs, cons
   a.causal = (pl->params.flags & RC_ATTN_CAUSAL) != 0;
   constexpr float kLog2e = 1.44269504088896340736f;
   a.scale = fminf((pl->params.scale > 0.0f ? pl->params.scale : 1.0f / sqrtf((float)s.head_dim)) * kLog2e, FLT_MAX);
-  const Way w = way_of(pl, {seqs, q_tokens, kv_tokens, a.max_q, a.max_kv, a.group}, pl->part_rows);
+  const Call c{seqs, q_tokens, kv_tokens, a.max_q, a.max_kv, a.group};
+  const Way w = way_of(pl, c, pl->part_rows);
+  if (most_threads(pl, c, w) >= (int64_t)1 << 32) return RC_ERR_UNSUPPORTED;  // a launch would run fewer, without an error
   a.splits = w.splits;
   a.direct = w.direct;
   a.chunk = w.chunk;

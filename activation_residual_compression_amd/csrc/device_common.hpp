@@ -8,6 +8,19 @@ namespace rc {
 
 constexpr int kWave = 64;
 
+// A launch takes fewer than 2^32 threads; of more it runs what is left of them modulo 2^32, without an error.
+// launch(first, blocks) for all `grid` blocks of up to 256 threads, 2^23 at a time.
+template <typename F>
+inline hipError_t launch_all(int64_t grid, F&& launch) {
+  constexpr int64_t most = (int64_t)1 << 23;
+  hipError_t err = hipSuccess;
+  for (int64_t first = 0; first < grid && err == hipSuccess; first += most) {
+    launch(first, (unsigned)(grid - first < most ? grid - first : most));
+    err = hipGetLastError();
+  }
+  return err;
+}
+
 // ---------------------------------------------------------------- DPP lanes
 // Cross-lane moves inside a row of 16 lanes, fused by the compiler into
 // v_mov_b32_dpp. The patterns used by the reductions:

@@ -77,10 +77,10 @@ __device__ __forceinline__ void copy_chunk(const PageGeom& g, const PageParts& f
 }
 
 __global__ __launch_bounds__(256) void pages_copy_kernel(PageGeom g, PageParts from, PageParts to, const int32_t* src,
-                                                         const int32_t* dst, int chunks) {
+                                                         const int32_t* dst, int chunks, int pair0, int chunk0) {
   // Blocks of threads go to the 8 XCDs in turn; each gets a run of the work (77 us, in turn 80).
   const int runs = gridDim.x / 8, w = (int)blockIdx.x < 8 * runs ? (int)blockIdx.x % 8 * runs + (int)blockIdx.x / 8 : (int)blockIdx.x;
-  const int i = w / chunks, chunk = w % chunks;
+  const int i = pair0 + (chunk0 + w) / chunks, chunk = (chunk0 + w) % chunks;
   const int p = src[i], q = dst[i];
   if ((unsigned)p >= (unsigned)g.pool_blocks || (unsigned)q >= (unsigned)g.pool_blocks) return;
   copy_chunk(g, from, to, p, q, chunk);
@@ -296,9 +296,10 @@ __global__ __launch_bounds__(kThreads) void pages_reserve_kernel(PageGeom g, Pag
   }
 }
 
-__global__ __launch_bounds__(256) void pages_pairs_kernel(PageGeom g, PageParts cache, const int2* pairs, int chunks) {
-  const int2 pair = pairs[blockIdx.x / chunks];
-  if (pair.x >= 0) copy_chunk(g, cache, cache, pair.x, pair.y, blockIdx.x % chunks);
+__global__ __launch_bounds__(256) void pages_pairs_kernel(PageGeom g, PageParts cache, const int2* pairs, int chunks, int64_t first) {
+  const uint32_t at = (uint32_t)first + blockIdx.x;  // slots * chunks: under 2^31
+  const int2 pair = pairs[at / chunks];
+  if (pair.x >= 0) copy_chunk(g, cache, cache, pair.x, pair.y, at % chunks);
 }
 
 // ------------------------------------------------------------------ fork, free
@@ -440,10 +441,9 @@ hipError_t launch_pages_reserve(const PageGeom& g, const PageWork& w, const Page
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const int chunks = chunks_of(g);
-  const int64_t grid = (int64_t)g.slots * chunks;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
-  pages_pairs_kernel<<<(unsigned)grid, 256, 0, s>>>(g, cache, w.pairs, chunks);
-  return hipGetLastError();
+  return launch_all((int64_t)g.slots * chunks, [&](int64_t first, unsigned blocks) {
+    pages_pairs_kernel<<<blocks, 256, 0, s>>>(g, cache, w.pairs, chunks, first);
+  });
 }
 
 hipError_t launch_pages_fork(const PageGeom& g, const PageWork& w, int32_t* refs, int32_t* table, const int32_t* source,
@@ -481,10 +481,9 @@ hipError_t launch_pages_compact(const PageGeom& g, const PageWork& w, const Page
 hipError_t launch_pages_copy(const PageGeom& g, const PageParts& from, const PageParts& to, const int32_t* src,
                              const int32_t* dst, int count, hipStream_t s) {
   const int chunks = chunks_of(g);
-  const int64_t grid = (int64_t)count * chunks;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
-  pages_copy_kernel<<<(unsigned)grid, 256, 0, s>>>(g, from, to, src, dst, chunks);
-  return hipGetLastError();
+  return launch_all((int64_t)count * chunks, [&](int64_t first, unsigned blocks) {
+    pages_copy_kernel<<<blocks, 256, 0, s>>>(g, from, to, src, dst, chunks, (int)(first / chunks), (int)(first % chunks));
+  });
 }
 
 }  // namespace rc

@@ -70,6 +70,8 @@ rc_status_t rc_attn_plan_create(rc_attn_shape_t shape, rc_dtype_t dtype, const r
  * offsets to find its rows); of a longer sequence only the first max_q queries and the first
  * max_kv keys are there. Rows of out and lse that belong to no sequence's queries stay
  * as they are.
+ * RC_ERR_UNSUPPORTED: a call that would take 2^24 blocks of threads or more: one at least for
+ * each key head of each sequence, and each 16 to 256 query rows (bound it by max_q).
  * lse (NULL, or fp32 [q_tokens][q_heads]): the natural logarithm of the sum of the
  * exponentials. A query that sees no key, or whose scores are all -infinity, gets 0 and
  * -infinity.

@@ -146,3 +146,14 @@ def test_every_part_has_a_block_in_plans_larger_than_the_call(lib, f32, causal):
             split += check_call(plan, lq, lk, *bounds)
         plan.close()
     assert split > 1000
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_calls_of_more_threads_than_a_launch_can_have_are_refused(lib, f32):
+    """2^32 threads: nothing is launched, neither in parts. 255 key heads of as many sequences are fewer."""
+    for heads, want in ((255, rc.RC_OK), (257, rc.RC_ERR_UNSUPPORTED)):
+        plan = Plan(lib, heads, heads, 64, 65535, 65535, 70000, f32)
+        for nq, nk, mq, mk in ((65535, 1000, 1, 1), (100, 1000, 100, 1000), (65535, 65535, 1, 1)):
+            status, w = plan.call(65535, nq, nk, mq, mk)
+            assert status == want and (w.kind != 0) == (want == rc.RC_OK), (heads, nq, nk)
+        plan.close()
