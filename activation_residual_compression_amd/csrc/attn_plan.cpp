@@ -346,7 +346,7 @@ rc_status_t rc_attn_join(hipStream_t stream, int parts, const rc_kv_view_t* outs
     return RC_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return RC_ERR_UNSUPPORTED;
   rc::AttnJoinArgs a;
-  const int64_t rows = (int64_t)batch * tokens * std::min<int64_t>(heads, 1 << 20);
+  const __int128 rows = (__int128)((int64_t)batch * tokens) * heads;  // up to 2^93
   for (int i = 0; i < parts; ++i) {
     const rc_status_t st = rows_of(&outs[i], batch, rows ? tokens : 0, heads, head_dim, false, &a.in[i]);
     if (st != RC_OK) return st;
@@ -364,7 +364,7 @@ rc_status_t rc_attn_join(hipStream_t stream, int parts, const rc_kv_view_t* outs
   a.tokens = tokens;
   a.heads = heads;
   a.dim = head_dim;
-  a.rows = rows;
+  a.rows = (int64_t)rows;
   return rc::launch_attn_join(a, outs[0].dtype == RC_BF16, out->dtype == RC_BF16, stream) == hipSuccess ? RC_OK
                                                                                                        : RC_ERR_HIP;
 }

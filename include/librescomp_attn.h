@@ -106,7 +106,8 @@ size_t rc_attn_workspace_bytes(rc_attn_plan_t plan);
  * NULL, or the same. head_dim: 64 or 128. out and lse may be those of one of the parts (the
  * same view), but not overlap them otherwise. A part of lse -infinity is left out, whatever
  * its outputs hold; where all are, out is 0 and lse -infinity. A part's lse of NaN or
- * +infinity makes both NaN. Sums are held in fp32. Needs no plan. */
+ * +infinity makes both NaN. Sums are held in fp32. Needs no plan. RC_ERR_UNSUPPORTED: another
+ * head_dim, more than 2^20 heads, 2^34 rows (batch * tokens * heads) or more. */
 rc_status_t rc_attn_join(hipStream_t stream, int parts, const rc_kv_view_t* outs, const float* const* lses,
                          int batch, int tokens, int heads, int head_dim, const rc_kv_view_t* out, float* lse);
 

@@ -157,3 +157,18 @@ def test_calls_of_more_threads_than_a_launch_can_have_are_refused(lib, f32):
             status, w = plan.call(65535, nq, nk, mq, mk)
             assert status == want and (w.kind != 0) == (want == rc.RC_OK), (heads, nq, nk)
         plan.close()
+
+
+def test_join_refuses_more_rows_than_it_can_count(lib):
+    """Also where the product of batch, tokens and heads passes 64 bits and is 0 or negative there."""
+    def join(batch, tokens, heads):
+        view = ctypes.byref(rc.rc_kv_view_t(A, rc.RC_BF16, 1 << 39, 64 * heads, 64))
+        lib.choice().contents.kind = 0
+        status = lib.rc_attn_join(None, 1, view, (ctypes.c_void_p * 1)(A), batch, tokens, heads, 64, view, A)
+        return status, lib.choice().contents.kind
+    assert join(1, 1 << 13, 1 << 20) == (rc.RC_OK, 4)
+    assert join(0, 1 << 30, 1 << 20) == (rc.RC_OK, 0)
+    for shape in ((2, 1 << 13, 1 << 20), (1, 1 << 14, 1 << 20), ((1 << 31) - 1, 1 << 29, 16)):
+        assert join(*shape) == (rc.RC_ERR_UNSUPPORTED, 0), shape
+    for shape in ((1 << 30, 1 << 30, 16), (1 << 30, 1 << 30, 1 << 20)):     # the batches would overlap too
+        assert join(*shape) == (rc.RC_ERR_INVALID_ARG, 0), shape
