@@ -258,7 +258,7 @@ rc_status_t rc_attn_plan_create(rc_attn_shape_t shape, rc_dtype_t dtype, const r
   const bool halved = dtype == RC_F32 && pl->many && (int64_t)shape.max_queries * (shape.q_heads / shape.kv_heads) > 64;
   pl->ws_bytes = up16(parts + counts) + (halved ? halves : 0);
   if (pl->ws_bytes) {
-    if (hipMalloc(&pl->ws, pl->ws_bytes) != hipSuccess) {
+    if (!rc::allocate(&pl->ws, pl->ws_bytes)) {
       delete pl;
       return RC_ERR_HIP;
     }

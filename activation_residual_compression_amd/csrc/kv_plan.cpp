@@ -232,7 +232,7 @@ rc_status_t rc_kv_plan_create(rc_kv_shape_t shape, rc_dtype_t dtype, const rc_kv
   pl->part_rows = part_rows_at_most(pl);
   if (pl->part_rows) {
     const size_t parts = part_bytes(pl, pl->part_rows), counts = kFewGroups * sizeof(uint32_t);
-    if (hipMalloc(&pl->ws, parts + counts) != hipSuccess) {
+    if (!rc::allocate(&pl->ws, parts + counts)) {
       delete pl;
       return RC_ERR_HIP;
     }

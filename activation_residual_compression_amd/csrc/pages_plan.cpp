@@ -79,7 +79,7 @@ rc_status_t rc_pages_plan_create(rc_pages_shape_t shape, rc_pages_plan_t* out) {
   pl->ws_bytes = carve(pl, nullptr);
   const size_t pool = (size_t)shape.pool_blocks;
   // done before the first call, which may be on a stream that does not wait for this one
-  if (hipMalloc(&pl->ws, pl->ws_bytes) != hipSuccess) {
+  if (!rc::allocate(&pl->ws, pl->ws_bytes)) {
     delete pl;
     return RC_ERR_HIP;
   }

@@ -10,6 +10,7 @@
 #include "../../include/librescomp.h"
 #include "../../include/librescomp_diag.h"
 #include "launch.hpp"
+#include "memory.hpp"
 
 struct rc_plan {
   rc_shape_t shape;
@@ -183,8 +184,7 @@ rc_status_t setup_lowrank(rc_plan* pl, const float* q0) {
   const int64_t total = rc::carve_lowrank(&w, pl->shape, pl->params, nullptr);
   hipError_t err = hipGetDevice(&pl->device);
   if (err != hipSuccess) return RC_ERR_HIP;
-  err = hipMalloc(&pl->ws, (size_t)total);
-  if (err != hipSuccess) { pl->ws = nullptr; return RC_ERR_HIP; }
+  if (!rc::allocate(&pl->ws, (size_t)total)) return RC_ERR_HIP;
   pl->ws_bytes = (size_t)total;
   rc::carve_lowrank(&w, pl->shape, pl->params, pl->ws);
   const int64_t kp = w.pay_rank, k = w.rank;
@@ -228,7 +228,7 @@ rc_status_t setup_blocksel(rc_plan* pl) {
       keep_prev ? align_up(B * pl->layout.n * (pl->dtype == RC_BF16 ? 2 : 4)) : 0;
   const int64_t total = score_bytes + state_bytes + prev_bytes;
   if (hipGetDevice(&pl->device) != hipSuccess) return RC_ERR_HIP;
-  if (hipMalloc(&pl->ws, (size_t)total) != hipSuccess) { pl->ws = nullptr; return RC_ERR_HIP; }
+  if (!rc::allocate(&pl->ws, (size_t)total)) return RC_ERR_HIP;
   pl->ws_bytes = (size_t)total;
   pl->bs_score = static_cast<double*>(pl->ws);
   pl->bs_visited = static_cast<uint8_t*>(pl->ws) + score_bytes;
@@ -379,9 +379,7 @@ rc_status_t rc_plan_create(rc_shape_t shape, rc_dtype_t dtype, rc_scheme_t schem
     if (st != RC_OK) { rc_plan_destroy(pl); return st; }
   }
   if (params->flags & (RC_CHECK_FINITE | RC_LR_CHECK_NUMERIC)) {
-    if (hipGetDevice(&pl->device) != hipSuccess ||
-        hipMalloc((void**)&pl->check, sizeof(uint32_t)) != hipSuccess) {
-      pl->check = nullptr;
+    if (hipGetDevice(&pl->device) != hipSuccess || !rc::allocate((void**)&pl->check, sizeof(uint32_t))) {
       rc_plan_destroy(pl);
       return RC_ERR_HIP;
     }

@@ -5,6 +5,7 @@
 #include <algorithm>
 
 #include "kv.hpp"
+#include "memory.hpp"
 
 namespace rc {
 
