@@ -229,7 +229,7 @@ __global__ __launch_bounds__(64 * WAVES, F32 || D == 128 || WAVES == 8 ? 2 : 3) 
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        p[t][i] = exp2_fast(fmaf(s4[t][i], a.scale, -m_run));
+        p[t][i] = exp2_fast(s4[t][i] * a.scale - m_run);  // the product rounded like m, or they differ by up to half a step of it
         l_run += p[t][i];
       }
     if (strange) {  // values that are not finite become zero

@@ -36,6 +36,7 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr float kMost = 0x1p10f;
+constexpr float kFine = 0x1p20f;  // up to here S c and its rounding differ by 2^-4 at most
 
 template <int D, int U, int KG>
 __global__ __launch_bounds__(256 * KG, 2) void attn_many_kernel(AttnArgs a) {
@@ -100,6 +101,7 @@ __global__ __launch_bounds__(256 * KG, 2) void attn_many_kernel(AttnArgs a) {
   // rows of this wave, and its queries: operand f has channels 16 f + 8 half + 0..7
   bf16x8 q[U][NK];
   float m_run[U], l_run[U];
+  float most = kMost;  // -1 when some row's m is past kFine
   int wave_lo = INT32_MAX, my_tiles = 0;  // keys that all its rows see, tiles that one does
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -163,6 +165,17 @@ __global__ __launch_bounds__(256 * KG, 2) void attn_many_kernel(AttnArgs a) {
       p[(i + k) / 8][(i + k) % 8 / 2] = w;
     }
   };
+  // The same with S c rounded like m: from 2^30 on their difference would take the weights out of fp32.
+  const auto weigh_rounded = [&](const f32x16& s, int u, float& sum, u32x4 (&p)[2]) {
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float x = exp2_fast(s[i] * a.scale - m_run[u]), y = exp2_fast(s[i + 1] * a.scale - m_run[u]);
+      sum += x + y;
+      p[i / 8][i % 8 / 2] = bf16_pair(x, y);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
   const auto weigh_all = [&](const f32x16& s, int u, float& sum, u32x4 (&p)[2]) {
     sum = 0.0f;
 #pragma unroll
@@ -172,7 +185,7 @@ __global__ __launch_bounds__(256 * KG, 2) void attn_many_kernel(AttnArgs a) {
     }
   };
   const auto settle = [&](const f32x16& s, int u, float& sum, u32x4 (&p)[2]) {  // whether m has to rise
-    if (__any(sum > kMost)) {
+    if (__any(!(sum <= most))) {
       float top = s[0];
 #pragma unroll
       for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
@@ -183,7 +196,10 @@ __global__ __launch_bounds__(256 * KG, 2) void attn_many_kernel(AttnArgs a) {
       for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int k = 0; k < 16; ++k) o[u][d][k] *= alpha;
-      weigh_all(s, u, sum, p);
+      const bool coarse = most != kMost || __any(fabsf(m_new) > kFine && m_new != kLowest);
+      most = coarse ? -1.0f : kMost;
+      if (coarse) weigh_rounded(s, u, sum, p);
+      else weigh_all(s, u, sum, p);
     }
     l_run[u] += sum;
   };

@@ -31,6 +31,7 @@ namespace rc {
 namespace {
 
 constexpr float kMost = 0x1p15f, kAbove = 8.0f;  // log2 of the largest weight after m is raised
+constexpr float kFine = 0x1p20f;                 // up to here a score and its rounding differ by 2^-4 at most
 constexpr int kExp = 14, kLeast = -90;  // exponent of a row's largest value; e is not below kLeast
 constexpr int kBias = 27;               // the factor of a key is 2^(e - kBias), so that it does not take a score out of fp32
 
@@ -110,6 +111,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
   constexpr int STEP = 256 / PER, C = KEYS / STEP;  // rows of a load of all threads, loads of a thread for K1
   __shared__ __align__(1024) char shared[2 * BYTES];
   __shared__ __align__(1024) float powers[2][2][KEYS];  // [buffer][K, V]
+  __shared__ int shifts[ROWS];  // used by one wave each
   const auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
   const uint32_t all = gridDim.x / a.splits, w = blockIdx.x % all;
   const int split = a.splits - 1 - (int)(blockIdx.x / all);
@@ -196,6 +198,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
   }
   const bool odd_rows = __any(odd_row);
   float m_run = kLowest, l_run = 0.0f;
+  float most = kMost;  // -1 when some row's m is past kFine: its outputs are held as 2^-shifts of what they are
   int wave_lo = INT32_MAX, my_tiles = 0;  // keys that all its rows see, tiles that one does
   {
     const int first = r0 + 32 * wave, last = min(first + 32, rows) - 1;
@@ -285,22 +288,61 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  const auto settle = [&](const f32x16& s, const f32x4 (&fk)[4], const f32x4 (&fv)[4], float& sum, float& heavy, u32x4 (&p1)[2], u32x4 (&p2)[2]) {
-    if (__any(heavy > kMost)) {
-      float top = -INFINITY;
+  // Whether m has to rise. For large scores fp32 is too coarse for an m that follows p 2^ev (from 2^27 on no such m makes
+  // all weights fit f16): m is then the largest score, rounded like all of them, and a power of two of the row's own
+  // brings its weights into f16.
+  const auto settle = [&](const f32x16& s, const f32x4 (&fk)[4], const f32x4 (&fv)[4], float& sum, float heavy, u32x4 (&p1)[2], u32x4 (&p2)[2]) {
+    if (__any(heavy > most)) {
+      const auto score = [&](int i) { return s[i] * fabsf(fk[i / 4][i % 4]); };  // without the factor
+      float high = -INFINITY, top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-  #pragma unroll
-        for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaf(s[i + k] * fabsf(fk[i / 4][k]), factor, exponent_of(fv[i / 4][k])));
+      for (int i = 0; i < 16; ++i) {
+        const float t = score(i) * factor;
+        high = fmaxf(high, t);
+        top = fmaxf(top, t + exponent_of(fv[i / 4][i % 4]));
+        __builtin_amdgcn_sched_barrier(0);
       }
-      const float m_new = fmaxf(m_run, max_halves(top) - kAbove), alpha = exp2_fast(m_run - m_new);
-      l_run *= alpha;
+      float m_new = fmaxf(m_run, max_halves(top) - kAbove);
+      const bool was = most != kMost, coarse = was || __any(fabsf(m_new) > kFine && m_new != kLowest);
+      most = coarse ? -1.0f : kMost;
+      int shift = 0, now = 0;
+      if (coarse) {
+        int* const at = &shifts[thread_again() / 64 * 32 + (thread_again() & 31)];
+        shift = was ? *at : 0;
+        m_new = fmaxf(m_run, max_halves(high));
+        top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          top = fmaxf(top, score(i) * factor - m_new + exponent_of(fv[i / 4][i % 4]));
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        // 2^13 for the largest weight of these keys, or what is left of the largest before
+        now = max((int)fmaxf(max_halves(top), -200.0f) - 13, shift + (int)fmaxf(m_run - m_new, -1000.0f));
+        *at = now;
+      }
+      const float down = m_run - m_new, alpha = exp2_fast(down + (float)(shift - now));
+      l_run *= exp2_fast(down);
       m_run = m_new;
 #pragma unroll
       for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int k = 0; k < 16; ++k) o[d][k] *= alpha;
-      weigh_all(s, fk, fv, sum, heavy, p1, p2);
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        float e[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          e[k] = exp2_fast(score(i + k) * factor - m_run);
+          sum += e[k];
+          e[k] = ldexpf(e[k], -now) * fabsf(fv[i / 4][i % 4 + k]);
+        }
+        uint32_t hi, lo;
+        split_pair(e[0], e[1], hi, lo);
+        p1[i / 8][i % 8 / 2] = hi;
+        p2[i / 8][i % 8 / 2] = lo;
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     l_run += sum;
   };
@@ -369,6 +411,14 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
   const int64_t slot = (int64_t)w * a.splits + split;  // of partial results
   const int again = thread_again(), lane_ = again & 63, half_ = lane_ >> 5, row = r0 + 32 * wave + (lane_ & 31);
   const float l = sum_halves(l_run), inv = attn_inverse(l);
+  if (most != kMost) {
+    const int shift = shifts[32 * wave + (lane_ & 31)];
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) o[d][k] = ldexpf(parts > 1 ? o[d][k] : o[d][k] * inv, shift);
+  }
+  const float last = parts > 1 || most != kMost ? 1.0f : inv;
   f32x4* const part = reinterpret_cast<f32x4*>(a.part) + (slot * (ROWS / 32) + wave) * ND * 4 * 64 + lane_;
   const int query = sq.q0 + row / a.group, head = h * a.group + row % a.group;
   const bool live = row < rows;
@@ -381,7 +431,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = o[d][4 * c + e];
       if (parts > 1) part[(d * 4 + c) * 64] = x;  // as the lanes hold them
-      else if (live) *reinterpret_cast<f32x4*>(out + 32 * d + 8 * c) = x * inv;
+      else if (live) *reinterpret_cast<f32x4*>(out + 32 * d + 8 * c) = x * last;
     }
   if (live && half_ == 0) {
     if (parts > 1) a.part_ml[slot * ROWS + 32 * wave + lane_] = make_float2(m_run, l);

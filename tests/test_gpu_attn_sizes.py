@@ -1,0 +1,61 @@
+"""Attention over packed sequences at the ends of fp32's range: scores that are larger than what separates them from the
+running maximum can be, and in fp32, whose kernel for many rows takes each factor as two f16 on a power of two of its row,
+queries, keys and values near both ends. Against attention in 64 bits (attn_dense, which derives the bounds)."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_harness import DEV, say
+from test_gpu_attn import DT, ints, rows, run, wide
+from test_gpu_attn_many import is_many
+from activation_residual_compression_amd import librescomp as rc
+
+pytestmark = pytest.mark.gpu
+DTYPES = pytest.mark.parametrize("dtype", ["bf16", "f32"])
+# few rows, in one part and in several; many, the keys in one part, in several
+SIZES = pytest.mark.parametrize("dim,nq,nk", [(64, 7, 300), (128, 5, 9000), (64, 1900, 1900), (128, 200, 9000)])
+
+
+@DTYPES
+@SIZES
+@pytest.mark.parametrize("power", [10, 20, 30, 90])
+def test_large_scores_choose_one_key(dtype, dim, nq, nk, power):
+    """Scores are +-2^power * 0, 1, 2, ... in some order, all exact: each row's output is the value of its largest one seen,
+    its lse that score (the next one is 2^10 / sqrt(128) lower at least, a weight of 2^-127 or less). Bounds: in bf16 the
+    weight's rounding (it is 2^r for the r that the score differs from its own rounding by) and the output's, in fp32
+    products of 22 bits; the lse's product with the scale and its two roundings."""
+    assert is_many([nq], [nk], 2, 2, dim) == (nq > 100)
+    rng = np.random.default_rng(power)
+    say("[gpu] one key, 2^%d %s %s" % (power, dtype, (dim, nq, nk)))
+    order = rng.permutation(nk)
+    q, k = np.zeros((nq, 2, dim)), np.zeros((nk, 2, dim))
+    sign = rng.choice([-1.0, 1.0], (nq, 2))
+    q[:, :, 3], q[:, :, dim - 1] = sign * 128 * 2.0 ** (power // 2), sign * 2.0 ** (power // 2)
+    k[:, :, 3], k[:, :, dim - 1] = (order // 128 * 2.0 ** (power - power // 2))[:, None], (order % 128 * 2.0 ** (power - power // 2))[:, None]
+    q, k = (torch.from_numpy(x).to(DT[dtype]).to(DEV) for x in (q, k))
+    v = rows(rng, nk, 2, dim, dtype)
+    for causal in (False, True):
+        out, lse = torch.full_like(q, float("nan")), torch.full((nq, 2), float("nan"), device=DEV)
+        with rc.AttnPlan(2, 2, dim, dtype, max_seqs=1, max_queries=nq, max_keys=nk, causal=causal) as p:
+            p.attend(q, k, v, ints([0, nq]), out, lse, kv_offsets=ints([0, nk]))
+            torch.cuda.synchronize()
+        seen = np.arange(nk - nq + 1, nk + 1) if causal else np.full(nq, nk)
+        high, low = np.maximum.accumulate(order)[seen - 1], np.minimum.accumulate(order)[seen - 1]
+        best = np.where(sign > 0, high[:, None], low[:, None])
+        at = np.empty(nk, int)
+        at[order] = np.arange(nk)
+        want = wide(v)[at[best], np.arange(2)]
+        assert (np.abs(wide(out) - want) <= np.abs(want) * (2 * 2.0 ** -8 if dtype == "bf16" else 2.0 ** -20)).all()
+        score = sign * best * 2.0 ** power / np.sqrt(dim)
+        assert (np.abs(wide(lse) - score) <= np.abs(score) * 2.0 ** -21).all()
+
+
+@DTYPES
+@SIZES
+@pytest.mark.parametrize("up,down", [(20, 6), (20, 12), (40, -4), (60, 50)])
+def test_large_scores_stay_finite(dtype, dim, nq, nk, up, down):
+    rng = np.random.default_rng(up)
+    say("[gpu] scores of 2^%d %s %s" % (up + down, dtype, (dim, nq, nk)))
+    q, k, v = rows(rng, nq, 2, dim, dtype) * 2.0 ** up, rows(rng, nk, 2, dim, dtype) * 2.0 ** down, rows(rng, nk, 2, dim, dtype)
+    for causal in (False, True):
+        run(q, k, v, [nq], [nk], causal, dtype)
