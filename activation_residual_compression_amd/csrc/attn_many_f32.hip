@@ -111,7 +111,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
   constexpr int STEP = 256 / PER, C = KEYS / STEP;  // rows of a load of all threads, loads of a thread for K1
   __shared__ __align__(1024) char shared[2 * BYTES];
   __shared__ __align__(1024) float powers[2][2][KEYS];  // [buffer][K, V]
-  __shared__ int shifts[ROWS];  // used by one wave each
+  __shared__ int shifts[ROWS], lifts[ROWS];  // used by one wave each; lifts: the power of two that `factor` lacks
   const auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
   const uint32_t all = gridDim.x / a.splits, w = blockIdx.x % all;
   const int split = a.splits - 1 - (int)(blockIdx.x / all);
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
   const int r = min(r0 + 32 * wave + col, rows - 1);
   half8_t q1[NK], q2[NK];
   float factor;  // of the scores: the row's 2^e and the plan's
-  bool odd_row = false;
+  bool odd_row = false, lifted;
   {
     const float* p = (const float*)a.q.data + (int64_t)(sq.q0 + r / a.group) * a.q.st + (int64_t)(h * a.group + r % a.group) * a.q.sh;
     uint32_t top = 0;
@@ -179,7 +179,11 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
     odd_row = top >= 0x7F800000u;
     const int e = odd_row ? 0 : row_exponent(top);
     const float inv = odd_row ? 0.0f : power_of_2(-e);
-    factor = fminf(power_of_2(e) * 0x1p27f * a.scale, 0x1p127f);
+    // Queries of 2^115 and more, with the keys' bias, can take it out of fp32: what passes 2^127 is kept apart.
+    const int lift = max(e + kBias + (int)exponent_of(a.scale) - 126, 0);
+    factor = ldexpf(a.scale, e + kBias - lift);
+    if (half == 0) lifts[32 * wave + col] = lift;
+    lifted = __any(lift > 0);
 #pragma unroll
     for (int f = 0; f < NK; ++f) {
       u32x4 hi, lo;
@@ -196,7 +200,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
       q2[f] = __builtin_bit_cast(half8_t, lo);
     }
   }
-  const bool odd_rows = __any(odd_row);
+  const bool odd_rows = __any(odd_row), uneven = odd_rows || lifted;
   float m_run = kLowest, l_run = 0.0f;
   float most = kMost;  // -1 when some row's m is past kFine: its outputs are held as 2^-shifts of what they are
   int wave_lo = INT32_MAX, my_tiles = 0;  // keys that all its rows see, tiles that one does
@@ -373,9 +377,14 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
       s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k1, q1[f], s, 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
     }
-    const int again = thread_again() & 63, half = again >> 5;
+    const int again = thread_again(), half = again >> 5 & 1;
     const uint64_t odd = __ballot(pow[(again & 31) + half * KEYS] < 0.0f);
-    if (odd_rows || (uint32_t)odd) odd_scores(s, first, (uint32_t)odd);
+    if (uneven || (uint32_t)odd) {
+      const int lift = lifts[again / 64 * 32 + (again & 31)];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = ldexpf(s[i], lift);
+      if (odd_rows || (uint32_t)odd) odd_scores(s, first, (uint32_t)odd);
+    }
     hide(s, first);
     n1 = value(tile, 0);
     n2 = value(tile + PLANE, 0);

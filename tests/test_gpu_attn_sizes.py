@@ -59,3 +59,17 @@ def test_large_scores_stay_finite(dtype, dim, nq, nk, up, down):
     q, k, v = rows(rng, nq, 2, dim, dtype) * 2.0 ** up, rows(rng, nk, 2, dim, dtype) * 2.0 ** down, rows(rng, nk, 2, dim, dtype)
     for causal in (False, True):
         run(q, k, v, [nq], [nk], causal, dtype)
+
+
+@pytest.mark.parametrize("dim,nq,nk", [(64, 1900, 1900), (128, 200, 9000)])
+@pytest.mark.parametrize("up,down", [(118, -70), (124, -60)])
+def test_large_queries(dim, nq, nk, up, down):
+    """The queries' power of two and the plan's factor pass fp32, the scores do not: each row's lse is its largest score."""
+    rng = np.random.default_rng(up)
+    say("[gpu] queries of 2^%d, keys of 2^%d, %d" % (up, down, dim))
+    q, k, v = (rows(rng, n, 2, dim, "f32") * 2.0 ** x for n, x in ((nq, up), (nk, down), (nk, 0)))
+    q[5] = 0
+    q[7] *= 2.0 ** -90
+    for causal in (False, True):
+        run(q, k, v, [nq], [nk], causal, "f32")
+    run(q * 2.0 ** -60, k * 2.0 ** -10, v, [nq], [nk], False, "f32", scale=2.0 ** 68)
