@@ -179,9 +179,10 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
     odd_row = top >= 0x7F800000u;
     const int e = odd_row ? 0 : row_exponent(top);
     const float inv = odd_row ? 0.0f : power_of_2(-e);
-    // Queries of 2^115 and more, with the keys' bias, can take it out of fp32: what passes 2^127 is kept apart.
+    // Queries of 2^115 and more, with the keys' bias, can take it out of fp32: what passes 2^127 is kept apart. And it is
+    // not 0 for a small one, as a hidden score, -infinity, times 0 is NaN.
     const int lift = max(e + kBias + (int)exponent_of(a.scale) - 126, 0);
-    factor = ldexpf(a.scale, e + kBias - lift);
+    factor = fmaxf(ldexpf(a.scale, e + kBias - lift), 0x1p-149f);
     if (half == 0) lifts[32 * wave + col] = lift;
     lifted = __any(lift > 0);
 #pragma unroll

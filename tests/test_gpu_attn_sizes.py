@@ -73,3 +73,14 @@ def test_large_queries(dim, nq, nk, up, down):
     for causal in (False, True):
         run(q, k, v, [nq], [nk], causal, "f32")
     run(q * 2.0 ** -60, k * 2.0 ** -10, v, [nq], [nk], False, "f32", scale=2.0 ** 68)
+
+
+@DTYPES
+@SIZES
+def test_small_scale(dtype, dim, nq, nk):
+    """A factor of the scores under fp32's normal range: all weights are 1, hidden keys stay hidden."""
+    rng = np.random.default_rng(nq)
+    say("[gpu] scale 2^-126 %s %s" % (dtype, (dim, nq, nk)))
+    q, k, v = rows(rng, nq, 2, dim, dtype) * 2.0 ** -50, rows(rng, nk, 2, dim, dtype), rows(rng, nk, 2, dim, dtype)
+    for causal in (False, True):
+        run(q, k, v, [nq], [nk], causal, dtype, scale=2.0 ** -126)
