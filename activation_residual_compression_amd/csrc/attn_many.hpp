@@ -218,8 +218,9 @@ __global__ __launch_bounds__(256) void attn_many_join_kernel(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (i0 + i >= parts) break;
-      const float f = exp2_fast(ml[i0 + i].x - m);
-      l += ml[i0 + i].y * f;
+      // In fp32 m follows the values too: the factor of a sum that counts can be under fp32's range, its root is not.
+      const float root = F32 ? exp2_fast(0.5f * (ml[i0 + i].x - m)) : 1.0f, f = F32 ? root * root : exp2_fast(ml[i0 + i].x - m);
+      l += F32 ? ml[i0 + i].y * root * root : ml[i0 + i].y * f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[c] += z[i][c] * f;
     }

@@ -32,6 +32,7 @@ namespace {
 
 constexpr float kMost = 0x1p15f, kAbove = 8.0f;  // log2 of the largest weight after m is raised
 constexpr float kFine = 0x1p20f;                 // up to here a score and its rounding differ by 2^-4 at most
+constexpr float kNear = 60.0f;                   // p is 2^-60 to 2^60 for the largest scores, and a rise of m less
 constexpr int kExp = 14, kLeast = -90;  // exponent of a row's largest value; e is not below kLeast
 constexpr int kBias = 27;               // the factor of a key is 2^(e - kBias), so that it does not take a score out of fp32
 
@@ -203,7 +204,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
   }
   const bool odd_rows = __any(odd_row), uneven = odd_rows || lifted;
   float m_run = kLowest, l_run = 0.0f;
-  float most = kMost;  // -1 when some row's m is past kFine: its outputs are held as 2^-shifts of what they are
+  float most = kMost;  // -1 when m is the largest score, for some row: outputs are held as 2^-shifts of what they are
   int wave_lo = INT32_MAX, my_tiles = 0;  // keys that all its rows see, tiles that one does
   {
     const int first = r0 + 32 * wave, last = min(first + 32, rows) - 1;
@@ -293,9 +294,10 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // Whether m has to rise. For large scores fp32 is too coarse for an m that follows p 2^ev (from 2^27 on no such m makes
-  // all weights fit f16): m is then the largest score, rounded like all of them, and a power of two of the row's own
-  // brings its weights into f16.
+  // Whether m has to rise. Where values are so large or small that an m that follows p 2^ev is far from the scores, p or
+  // what is left of l when m rises would leave fp32; for large scores fp32 is too coarse for such an m (from 2^27 on none
+  // makes all weights fit f16). m is then the largest score, rounded like all of them, and a power of two of the row's
+  // own brings its weights into f16.
   const auto settle = [&](const f32x16& s, const f32x4 (&fk)[4], const f32x4 (&fv)[4], float& sum, float heavy, u32x4 (&p1)[2], u32x4 (&p2)[2]) {
     if (__any(heavy > most)) {
       const auto score = [&](int i) { return s[i] * fabsf(fk[i / 4][i % 4]); };  // without the factor
@@ -308,13 +310,15 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
         __builtin_amdgcn_sched_barrier(0);
       }
       float m_new = fmaxf(m_run, max_halves(top) - kAbove);
-      const bool was = most != kMost, coarse = was || __any(fabsf(m_new) > kFine && m_new != kLowest);
+      high = max_halves(high);
+      const bool far = fabsf(m_new - high) > kNear || (m_run != kLowest && m_new - m_run > kNear);
+      const bool was = most != kMost, coarse = was || __any(m_new != kLowest && (fabsf(m_new) > kFine || far));
       most = coarse ? -1.0f : kMost;
       int shift = 0, now = 0;
       if (coarse) {
         int* const at = &shifts[thread_again() / 64 * 32 + (thread_again() & 31)];
         shift = was ? *at : 0;
-        m_new = fmaxf(m_run, max_halves(high));
+        m_new = fmaxf(m_run, high);
         top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {

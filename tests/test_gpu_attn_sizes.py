@@ -84,3 +84,26 @@ def test_small_scale(dtype, dim, nq, nk):
     q, k, v = rows(rng, nq, 2, dim, dtype) * 2.0 ** -50, rows(rng, nk, 2, dim, dtype), rows(rng, nk, 2, dim, dtype)
     for causal in (False, True):
         run(q, k, v, [nq], [nk], causal, dtype, scale=2.0 ** -126)
+
+
+@pytest.mark.parametrize("dim,nq,nk", [(64, 1900, 1900), (128, 200, 9000)])
+@pytest.mark.parametrize("what", ["small, then large", "large, then small", "any", "small after rising scores"])
+def test_values_of_very_different_sizes(dim, nq, nk, what):
+    """Tokens whose values differ by more than fp32 has powers of two between 1 and its end: each counts in the sum of the
+    weights, and so in lse, by its score alone."""
+    rng = np.random.default_rng(dim)
+    say("[gpu] values %s %d" % (what, dim))
+    q, k, v = (rows(rng, n, 2, dim, "f32") for n in (nq, nk, nk))
+    at = torch.arange(nk, device=DEV)[:, None, None]
+    if what == "any":
+        power = torch.from_numpy(rng.integers(-75, 110, (nk, 1, 1))).to(DEV)
+    elif what == "small after rising scores":            # weights of 1, then of 2^80 and more, then large values
+        q, k = q * 0.1, k * 0.1
+        q[:, :, 3] = 8.0
+        k[:, :, 3] = torch.where(at[:, :, 0] > nk // 3, 7.0 * dim ** 0.5, 0.0)
+        power = torch.where(at < nk // 3, 0, torch.where(at < nk // 2, -75, 60))
+    else:
+        power = torch.where((at < nk // 2) == (what[0] == "s"), -75, 100)
+    v = v * torch.exp2(power.float())
+    for causal in (False, True):
+        run(q, k, v, [nq], [nk], causal, "f32")
