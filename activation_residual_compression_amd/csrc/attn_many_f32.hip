@@ -2,8 +2,8 @@
 //
 // fp32 products on the f16 matrix units, which are 8.5 times as fast as those for fp32 (1196 and 141
 // TFLOP/s measured): x = 2^e (x1 + x2), x1 and x2 in f16 and e the row's own, so that its largest is
-// in [2^14, 2^15): 22 bits of each value down to 2^-17 of it, and to 2^-39 of it below. A product is
-// x1 y1 + x1 y2 + x2 y1; x2 y2, under 2^-22 of it, is left out.
+// in [2^14, 2^15): 22 bits of each value down to 2^-17 of it, and to 2^-39 of it below (to 2^-146 in
+// all, as e is not under -122). A product is x1 y1 + x1 y2 + x2 y1; x2 y2, under 2^-22 of it, is left out.
 //
 // The split of K and V is done once for all rows that read them, by a kernel before, into the
 // plan's workspace: [K1, K2, V1, V2][key head][token][D], and 2^e of each token's K and V. Values that
@@ -13,7 +13,8 @@
 // The attention is that of the kernel for bf16 (S^T = K Q^T, O^T = V^T P^T, tiles past the
 // registers into two LDS buffers), with p = 2^(S 2^(eq + ek) c - m), of which l is the sum, and
 // w = p 2^ev as weights of V's halves: m is raised when a w passes 2^15, to where the largest is 2^8,
-// so that w fits f16 and is split like the rest (to 2^-33 of a row's largest).
+// so that w fits f16 and is split like the rest (to 2^-33 of a row's largest). For large scores, and
+// values of which a row's are far from 1, m is the largest score alone (see `settle`).
 //
 // Bound by the matrix units at the clock that the card's power allows (1.6 GHz): 8192 queries over
 // 8192 keys, 16 heads of 128: 1.60 ms, 344 TFLOP/s of attention, 1.03 PFLOP/s of f16 products (a large
@@ -33,8 +34,8 @@ namespace {
 constexpr float kMost = 0x1p15f, kAbove = 8.0f;  // log2 of the largest weight after m is raised
 constexpr float kFine = 0x1p20f;                 // up to here a score and its rounding differ by 2^-4 at most
 constexpr float kNear = 60.0f;                   // p is 2^-60 to 2^60 for the largest scores, and a rise of m less
-constexpr int kExp = 14, kLeast = -90;  // exponent of a row's largest value; e is not below kLeast
-constexpr int kBias = 27;               // the factor of a key is 2^(e - kBias), so that it does not take a score out of fp32
+constexpr int kExp = 14, kLeast = -122;  // exponent of a row's largest value; e is not below kLeast
+constexpr int kBias = 27;                // the factor of a key is 2^(e - kBias), so that it does not take a score out of fp32
 
 // log2 of 2^e, or of its negative.
 __device__ __forceinline__ float exponent_of(float x) { return (float)((int)(__float_as_uint(x) >> 23 & 255u) - 127); }
@@ -99,7 +100,7 @@ __global__ __launch_bounds__(256) void attn_halves_kernel(AttnArgs a) {
   const int64_t to = ((2 * which) * rows + (int64_t)h * a.kv_tokens + token) * D + 8 * at;
   *reinterpret_cast<u32x4*>(a.halves + to) = hi;
   *reinterpret_cast<u32x4*>(a.halves + to + rows * D) = lo;
-  const float factor = power_of_2(which ? e : e - kBias);
+  const float factor = ldexpf(1.0f, which ? e : e - kBias);  // 2^-149 at least
   if (at == 0) a.powers[((int64_t)h * 2 + which) * a.kv_tokens + token] = odd ? -factor : factor;
 }
 
@@ -293,6 +294,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    heavy = fmaxf(heavy, sum * (kMost * 0x1p-100f));  // weights of tiny values may be small where p would leave fp32
   };
   // Whether m has to rise. Where values are so large or small that an m that follows p 2^ev is far from the scores, p or
   // what is left of l when m rises would leave fp32; for large scores fp32 is too coarse for such an m (from 2^27 on none
@@ -344,7 +346,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
         for (int k = 0; k < 2; ++k) {
           e[k] = exp2_fast(score(i + k) * factor - m_run);
           sum += e[k];
-          e[k] = ldexpf(e[k], -now) * fabsf(fv[i / 4][i % 4 + k]);
+          e[k] = ldexpf(ldexpf(e[k], -now / 2) * fabsf(fv[i / 4][i % 4 + k]), -now - -now / 2);
         }
         uint32_t hi, lo;
         split_pair(e[0], e[1], hi, lo);

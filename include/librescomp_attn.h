@@ -82,8 +82,8 @@ rc_status_t rc_attn_plan_create(rc_attn_shape_t shape, rc_dtype_t dtype, const r
  * values of 2^100 and more may overflow. In fp32 the factors of a product (q, k, v and the
  * weights) may be taken as sums of two f16, 22 bits each, on a scale of their row of head_dim
  * values: of a row's values under 2^-17 of its largest those bits are lost that lie under
- * 2^-39 of it, of weights (times the largest |v| of their token) those under 2^-33 of a
- * query's largest.
+ * 2^-39 of it, of all values those under 2^-146, of weights (times the largest |v| of their
+ * token) those under 2^-33 of a query's largest.
  * NaN and infinities: what a query does not see does not reach it, whatever it holds. A
  * NaN among the queries, or the keys that one sees, or a score of +infinity makes its
  * outputs and lse NaN; a value that is not finite makes the outputs that see it not finite. */

@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import attn_dense as ad
 from gpu_harness import DEV, say
 from test_gpu_attn import DT, ints, rows, run, wide
 from test_gpu_attn_many import is_many
@@ -107,3 +108,24 @@ def test_values_of_very_different_sizes(dim, nq, nk, what):
     v = v * torch.exp2(power.float())
     for causal in (False, True):
         run(q, k, v, [nq], [nk], causal, "f32")
+
+
+@pytest.mark.parametrize("dim,nq,nk", [(64, 1900, 1900), (128, 200, 9000)])
+@pytest.mark.parametrize("qp,kp,vp", [(110, -110, 0), (-110, 110, 0), (118, -118, 0), (0, 0, -85), (0, 0, -100), (0, 0, -116)])
+def test_rows_of_tiny_values(dim, nq, nk, qp, kp, vp):
+    """Queries, keys or values whose largest are far under 1 have the precision of others; checked with the values and
+    outputs, which are proportional, on a scale at which the bounds' absolute term is nothing."""
+    rng = np.random.default_rng(abs(dim - qp - vp))
+    say("[gpu] 2^%d 2^%d 2^%d, %d" % (qp, kp, vp, dim))
+    q, k, v = (rows(rng, n, 2, dim, "f32") * 2.0 ** x for n, x in ((nq, qp), (nk, kp), (nk, vp)))
+    up = torch.linspace(0, 100, nk, device=DEV)[:, None]
+    for rising in (False, True):                 # scores that rise by 140 and more in base 2, under small weights
+        if rising:
+            q[:, :, 1], k[:, :, 1] = dim ** 0.5 * 2.0 ** qp, up * 2.0 ** kp
+        for causal in (False, True):
+            out, lse = torch.full_like(q, float("nan")), torch.full((nq, 2), float("nan"), device=DEV)
+            with rc.AttnPlan(2, 2, dim, "f32", max_seqs=1, max_queries=nq, max_keys=nk, causal=causal) as p:
+                p.attend(q, k, v, ints([0, nq]), out, lse, kv_offsets=ints([0, nk]))
+                torch.cuda.synchronize()
+            ref = ad.attend(wide(q), wide(k), wide(v) * 2.0 ** -vp, causal, dim ** -0.5)
+            ad.check(wide(out) * 2.0 ** -vp, wide(lse), ref, nk, dim, True, (qp, kp, vp, rising, causal))
