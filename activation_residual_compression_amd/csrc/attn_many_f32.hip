@@ -33,8 +33,9 @@ namespace {
 
 constexpr float kMost = 0x1p15f, kAbove = 8.0f;  // log2 of the largest weight after m is raised
 constexpr float kFine = 0x1p20f;                 // up to here a score and its rounding differ by 2^-4 at most
-constexpr float kNear = 60.0f;                   // p is 2^-60 to 2^60 for the largest scores, and a rise of m less
+constexpr float kNear = 60.0f;                   // p is 2^-60 to 2^60 for the largest scores, a rise of m twice as much
 constexpr int kExp = 14, kLeast = -122;  // exponent of a row's largest value; e is not below kLeast
+constexpr int kNone = -126;              // of values that are all zero: their weight is none
 constexpr int kBias = 27;                // the factor of a key is 2^(e - kBias), so that it does not take a score out of fp32
 
 // log2 of 2^e, or of its negative.
@@ -86,7 +87,7 @@ __global__ __launch_bounds__(256) void attn_halves_kernel(AttnArgs a) {
   top = group_max_u32<LANES>(top);
   const uint32_t group = (threadIdx.x & 63) / LANES * LANES;
   odd = (__ballot(odd) >> group & ((1ull << LANES) - 1)) != 0;
-  const int e = row_exponent(top);
+  const int e = which && top == 0u ? kNone : row_exponent(top);
   const float inv = power_of_2(-e);
   u32x4 hi, lo;
 #pragma unroll
@@ -296,25 +297,30 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
     }
     heavy = fmaxf(heavy, sum * (kMost * 0x1p-100f));  // weights of tiny values may be small where p would leave fp32
   };
-  // Whether m has to rise. Where values are so large or small that an m that follows p 2^ev is far from the scores, p or
-  // what is left of l when m rises would leave fp32; for large scores fp32 is too coarse for such an m (from 2^27 on none
+  // Whether m has to rise. Where values are so large or small (or zero) that an m that follows p 2^ev is far from the
+  // scores, p or what is left of l when m rises would leave fp32; for large scores fp32 is too coarse for such an m (from 2^27 on none
   // makes all weights fit f16). m is then the largest score, rounded like all of them, and a power of two of the row's
   // own brings its weights into f16.
   const auto settle = [&](const f32x16& s, const f32x4 (&fk)[4], const f32x4 (&fv)[4], float& sum, float heavy, u32x4 (&p1)[2], u32x4 (&p2)[2]) {
     if (__any(heavy > most)) {
       const auto score = [&](int i) { return s[i] * fabsf(fk[i / 4][i % 4]); };  // without the factor
+      const auto weight = [&](float t, int i) {                                   // log2 of it
+        const float e = exponent_of(fv[i / 4][i % 4]);
+        return e == (float)kNone ? -INFINITY : t + e;
+      };
       float high = -INFINITY, top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float t = score(i) * factor;
         high = fmaxf(high, t);
-        top = fmaxf(top, t + exponent_of(fv[i / 4][i % 4]));
+        top = fmaxf(top, weight(t, i));
         __builtin_amdgcn_sched_barrier(0);
       }
-      float m_new = fmaxf(m_run, max_halves(top) - kAbove);
       high = max_halves(high);
-      const bool far = fabsf(m_new - high) > kNear || (m_run != kLowest && m_new - m_run > kNear);
-      const bool was = most != kMost, coarse = was || __any(m_new != kLowest && (fabsf(m_new) > kFine || far));
+      top = max_halves(top) - kAbove;
+      float m_new = fmaxf(m_run, top);
+      const bool far = high - kNear > m_new || (top > m_run && top - high > kNear) || (m_run != kLowest && m_new - m_run > 2.0f * kNear);
+      const bool was = most != kMost, coarse = was || __any(far || (m_new != kLowest && fabsf(m_new) > kFine));
       most = coarse ? -1.0f : kMost;
       int shift = 0, now = 0;
       if (coarse) {
@@ -324,11 +330,11 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
         top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          top = fmaxf(top, score(i) * factor - m_new + exponent_of(fv[i / 4][i % 4]));
+          top = fmaxf(top, weight(score(i) * factor - m_new, i));
           __builtin_amdgcn_sched_barrier(0);
         }
         // 2^13 for the largest weight of these keys, or what is left of the largest before
-        now = max((int)fmaxf(max_halves(top), -200.0f) - 13, shift + (int)fmaxf(m_run - m_new, -1000.0f));
+        now = max((int)fmaxf(max_halves(top), (float)kLeast) - 13, shift + (int)fmaxf(m_run - m_new, -1000.0f));
         *at = now;
       }
       const float down = m_run - m_new, alpha = exp2_fast(down + (float)(shift - now));

@@ -129,3 +129,27 @@ def test_rows_of_tiny_values(dim, nq, nk, qp, kp, vp):
                 torch.cuda.synchronize()
             ref = ad.attend(wide(q), wide(k), wide(v) * 2.0 ** -vp, causal, dim ** -0.5)
             ad.check(wide(out) * 2.0 ** -vp, wide(lse), ref, nk, dim, True, (qp, kp, vp, rising, causal))
+
+
+@pytest.mark.parametrize("dim,nq,nk", [(64, 1900, 1900), (128, 200, 9000)])
+@pytest.mark.parametrize("power", [0, -20, -40, -110])
+def test_values_beside_zeros(dim, nq, nk, power):
+    """Tokens whose values are all zero, at a sequence's start and among others: what the others add has its bits, however
+    small they are; checked on a scale at which the bounds' absolute term is nothing."""
+    rng = np.random.default_rng(dim - power)
+    say("[gpu] zeros and values of 2^%d, %d" % (power, dim))
+    q, k, v = (rows(rng, n, 2, dim, "f32") for n in (nq, nk, nk))
+    zero = torch.from_numpy(rng.random(nk) < 0.5).to(DEV)
+    zero[:300] = True
+    v = torch.where(zero[:, None, None], 0.0, v * 2.0 ** power)
+    # the zeros' scores are 72 above in base 2: outputs of 2^-72 times the values, which fp32 has for values of 2^-70 and more
+    for rising in (False, True) if power > -70 else (False,):
+        if rising:
+            q[:, :, 1], k[:, :, 1] = dim ** 0.5, torch.where(zero, 50.0, 0.0)[:, None]
+        for causal in (False, True):
+            out, lse = torch.full_like(q, float("nan")), torch.full((nq, 2), float("nan"), device=DEV)
+            with rc.AttnPlan(2, 2, dim, "f32", max_seqs=1, max_queries=nq, max_keys=nk, causal=causal) as p:
+                p.attend(q, k, v, ints([0, nq]), out, lse, kv_offsets=ints([0, nk]))
+                torch.cuda.synchronize()
+            ref = ad.attend(wide(q), wide(k), wide(v) * 2.0 ** -power, causal, dim ** -0.5)
+            ad.check(wide(out) * 2.0 ** -power, wide(lse), ref, nk, dim, True, (power, rising, causal))
