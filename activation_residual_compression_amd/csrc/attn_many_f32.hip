@@ -23,7 +23,10 @@
 // Three waves of a SIMD and tiles of 32 keys for D = 64 (4444 over 4444, 30 heads: 556 us, two waves
 // and 64 keys 585); the factors of a step's keys are read before its products (542). The products of
 // one half of a tile beside the weights of the other, as in the bf16 kernel: 559. On the fp32 matrix
-// units, by the kernel for few rows: 1566.
+// units, by the kernel for few rows: 1566. What the ends of fp32's range take (factors apart, sums that
+// show that weights leave it) does not show in large calls for heads of 128, is 1 % for heads of 64 and 3 %
+// of causal prompts in short parts; a wave whose m is the largest score weighs every step twice: 4096
+// over 4096, 16 heads of 128, 467 us for 414, of 64 351 for 238.
 #include <algorithm>
 
 #include "attn_many.hpp"
@@ -35,7 +38,7 @@ constexpr float kMost = 0x1p15f, kAbove = 8.0f;  // log2 of the largest weight a
 constexpr float kFine = 0x1p20f;                 // up to here a score and its rounding differ by 2^-4 at most
 constexpr float kNear = 60.0f;                   // p is 2^-60 to 2^60 for the largest scores, a rise of m twice as much
 constexpr int kExp = 14, kLeast = -122;  // exponent of a row's largest value; e is not below kLeast
-constexpr int kNone = -126;              // of values that are all zero: their weight is none
+constexpr int kNone = -126;              // of values that are all zero
 constexpr int kBias = 27;                // the factor of a key is 2^(e - kBias), so that it does not take a score out of fp32
 
 // log2 of 2^e, or of its negative.
@@ -304,10 +307,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
   const auto settle = [&](const f32x16& s, const f32x4 (&fk)[4], const f32x4 (&fv)[4], float& sum, float heavy, u32x4 (&p1)[2], u32x4 (&p2)[2]) {
     if (__any(heavy > most)) {
       const auto score = [&](int i) { return s[i] * fabsf(fk[i / 4][i % 4]); };  // without the factor
-      const auto weight = [&](float t, int i) {                                   // log2 of it
-        const float e = exponent_of(fv[i / 4][i % 4]);
-        return e == (float)kNone ? -INFINITY : t + e;
-      };
+      const auto weight = [&](float t, int i) { return t + exponent_of(fv[i / 4][i % 4]); };  // log2 of it
       float high = -INFINITY, top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
