@@ -14,8 +14,9 @@
 // both products are in fp32.
 //
 // Bound by HBM for long keys (one token of 64 sequences of 4000, 32 heads of 128 on 8: 181 us, 5.8
-// TB/s; of 65536 tokens 50 us, 5.3 TB/s, in fp32 99; 8 ragged ones of up to 32768 82 us, 4.7), by the
-// chain of reads for short ones (333 tokens, 24 heads: 8.1 us; 2048 tokens, 32 heads on 8: 9.4).
+// TB/s; of 65536 tokens 58 us, 4.6 TB/s, the same again and again 50, in fp32 99; 8 ragged ones of up to
+// 32768 82 us, 4.7), by the chain of reads for short ones (333 tokens, 24 heads: 8.1 us; 2048 tokens, 32
+// heads on 8: 9.4).
 // Blocks of threads of one piece and all key heads follow each other: their rows lie next to each
 // other in memory (65536 tokens with the pieces of a head after each other: 54 us).
 #include <type_traits>

@@ -16,12 +16,12 @@
 // so that w fits f16 and is split like the rest (to 2^-33 of a row's largest). For large scores, and
 // values of which a row's are far from 1, m is the largest score alone (see `settle`).
 //
-// Bound by the matrix units at the clock that the card's power allows (1.6 GHz): 8192 queries over
-// 8192 keys, 16 heads of 128: 1.60 ms, 344 TFLOP/s of attention, 1.03 PFLOP/s of f16 products (a large
-// one of the library: 1.20), the matrix units busy 60 % of the cycles; heads of 64: 0.98 ms, 49 %,
-// where the splitting of the weights (9 vector instructions each) takes as long as the products.
+// Bound by the matrix units at the clock that the card's power allows (1.8 GHz): 8192 queries over 8192
+// keys, 16 heads of 128: 1.45 ms, 379 TFLOP/s of attention, 1.14 PFLOP/s of f16 products (a large one of
+// the library: 1.21), the matrix units busy 65 % of the cycles; heads of 64: 0.83 ms, where the splitting
+// of the weights (9 vector instructions each) takes as long as the products.
 // Three waves of a SIMD and tiles of 32 keys for D = 64 (4444 over 4444, 30 heads: 556 us, two waves
-// and 64 keys 585); the factors of a step's keys are read before its products (542). The products of
+// and 64 keys 585); the factors of a step's keys are read before its products (542; now 515). The products of
 // one half of a tile beside the weights of the other, as in the bf16 kernel: 559. On the fp32 matrix
 // units, by the kernel for few rows: 1566. What the ends of fp32's range take (factors apart, sums that
 // show that weights leave it) does not show in large calls for heads of 128, is 1 % for heads of 64 and 3 %

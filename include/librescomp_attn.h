@@ -4,8 +4,8 @@
  *
  * Next to the 8-bit cache of librescomp_kv.h: whole prompts attend to their own
  * keys and values before these are stored, a GPU of a sequence-parallel step
- * attends to what is sent in full (step 0) or to its own share as it is, and the
- * result is joined with that of rc_kv_attend over the rest:
+ * attends to its own share as it is, and the result is joined with that of
+ * rc_kv_attend over the rest:
  *
  *   rc_attn_packed   attention of sequences of different lengths that lie one after
  *                    the other, without padding
