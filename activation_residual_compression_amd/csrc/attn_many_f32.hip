@@ -432,13 +432,23 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
 
   const int64_t slot = (int64_t)w * a.splits + split;  // of partial results
   const int again = thread_again(), lane_ = again & 63, half_ = lane_ >> 5, row = r0 + 32 * wave + (lane_ & 31);
-  const float l = sum_halves(l_run), inv = attn_inverse(l);
+  float l = sum_halves(l_run), inv = attn_inverse(l);
   if (most != kMost) {
     const int shift = shifts[32 * wave + (lane_ & 31)];
+    if (parts > 1) {  // the power goes into m, as far as m has the bits, or a sum of large values could leave fp32
+      const float m = m_run + fmaxf((float)shift, -kNear), by = m_run - m, root = exp2_fast(0.5f * ((float)shift + by));
+      m_run = m;
+      l *= exp2_fast(by);
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+      for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int k = 0; k < 16; ++k) o[d][k] = ldexpf(parts > 1 ? o[d][k] : o[d][k] * inv, shift);
+        for (int k = 0; k < 16; ++k) o[d][k] = o[d][k] * root * root;
+    } else {
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[d][k] = ldexpf(o[d][k] * inv, shift);
+    }
   }
   const float last = parts > 1 || most != kMost ? 1.0f : inv;
   f32x4* const part = reinterpret_cast<f32x4*>(a.part) + (slot * (ROWS / 32) + wave) * ND * 4 * 64 + lane_;

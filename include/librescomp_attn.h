@@ -78,12 +78,12 @@ rc_status_t rc_attn_plan_create(rc_attn_shape_t shape, rc_dtype_t dtype, const r
  * Precision: scores, sums, the running maximum and outputs are held in fp32 and rounded
  * once. In bf16 the weights may be rounded to bf16 (8 bits) for their product with v, not
  * for their sum: before the last rounding an output is within 2^-8 of the weighted mean of
- * |v|; sums of weights times values reach 2^10 times the number of keys times |v|, so that
- * values of 2^100 and more may overflow. In fp32 the factors of a product (q, k, v and the
- * weights) may be taken as sums of two f16, 22 bits each, on a scale of their row of head_dim
- * values: of a row's values under 2^-17 of its largest those bits are lost that lie under
- * 2^-39 of it, of all values those under 2^-146, of weights (times the largest |v| of their
- * token) those under 2^-33 of a query's largest.
+ * |v|; sums of weights times values reach 2^10 times the number of keys times |v| (in fp32 the
+ * number of keys times |v|), so that values of 2^100 and more may overflow. In fp32 the factors
+ * of a product (q, k, v and the weights) may be taken as sums of two f16, 22 bits each, on a
+ * scale of their row of head_dim values: of a row's values under 2^-17 of its largest those bits
+ * are lost that lie under 2^-39 of it, of all values those under 2^-146, of weights (times the
+ * largest |v| of their token) those under 2^-33 of a query's largest.
  * NaN and infinities: what a query does not see does not reach it, whatever it holds. A
  * NaN among the queries, or the keys that one sees, or a score of +infinity makes its
  * outputs and lse NaN; a value that is not finite makes the outputs that see it not finite. */

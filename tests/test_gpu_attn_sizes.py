@@ -153,3 +153,17 @@ def test_values_beside_zeros(dim, nq, nk, power):
                 torch.cuda.synchronize()
             ref = ad.attend(wide(q), wide(k), wide(v) * 2.0 ** -power, causal, dim ** -0.5)
             ad.check(wide(out) * 2.0 ** -power, wide(lse), ref, nk, dim, True, (power, rising, causal))
+
+
+@pytest.mark.parametrize("dim,nq,nk", [(64, 1900, 1900), (128, 200, 9000)])
+@pytest.mark.parametrize("power", [100, 118, 125])
+def test_huge_values(dim, nq, nk, power):
+    """Values of one sign whose sum over the keys passes fp32 and whose mean does not; also of large scores, of which one
+    key's value is the result."""
+    rng = np.random.default_rng(power)
+    say("[gpu] values of 2^%d, %d" % (power, dim))
+    q, k = rows(rng, nq, 2, dim, "f32"), rows(rng, nk, 2, dim, "f32")
+    v = (1 + torch.from_numpy(rng.random((nk, 2, dim)).astype(np.float32)).to(DEV)) * 2.0 ** power
+    for causal in (False, True):
+        run(q, k, v, [nq], [nk], causal, "f32")
+        run(q * 2.0 ** 15, k * 2.0 ** 15, v, [nq], [nk], causal, "f32")
