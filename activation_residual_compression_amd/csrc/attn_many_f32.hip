@@ -28,6 +28,7 @@
 // of causal prompts in short parts; a wave whose m is the largest score weighs every step twice: 4096
 // over 4096, 16 heads of 128, 467 us for 414, of 64 351 for 238.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_many.hpp"
 
@@ -301,9 +302,9 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
     heavy = fmaxf(heavy, sum * (kMost * 0x1p-100f));  // weights of tiny values may be small where p would leave fp32
   };
   // Whether m has to rise. Where values are so large or small (or zero) that an m that follows p 2^ev is far from the
-  // scores, p or what is left of l when m rises would leave fp32; for large scores fp32 is too coarse for such an m (from 2^27 on none
-  // makes all weights fit f16). m is then the largest score, rounded like all of them, and a power of two of the row's
-  // own brings its weights into f16.
+  // scores, p or what is left of l when m rises would leave fp32; for large scores fp32 is too coarse for such an m (from
+  // 2^27 on none makes all weights fit f16). m is then the largest score, rounded like all of them, and a power of two of
+  // the row's own brings its weights into f16.
   const auto settle = [&](const f32x16& s, const f32x4 (&fk)[4], const f32x4 (&fv)[4], float& sum, float heavy, u32x4 (&p1)[2], u32x4 (&p2)[2]) {
     if (__any(heavy > most)) {
       const auto score = [&](int i) { return s[i] * fabsf(fk[i / 4][i % 4]); };  // without the factor
@@ -344,22 +345,27 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_many_f32_kernel(Att
       for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int k = 0; k < 16; ++k) o[d][k] *= alpha;
-      sum = 0.0f;
+      const auto weigh_again = [&](auto apart) {
+        sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        float e[2];
+        for (int i = 0; i < 16; i += 2) {
+          float e[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          e[k] = exp2_fast(score(i + k) * factor - m_run);
-          sum += e[k];
-          e[k] = ldexpf(ldexpf(e[k], -now / 2) * fabsf(fv[i / 4][i % 4 + k]), -now - -now / 2);
+          for (int k = 0; k < 2; ++k) {
+            e[k] = exp2_fast(score(i + k) * factor - m_run);
+            sum += e[k];
+            const float v = fabsf(fv[i / 4][i % 4 + k]);
+            e[k] = decltype(apart)::value ? ldexpf(ldexpf(e[k], -now / 2) * v, -now - -now / 2) : e[k] * v;
+          }
+          uint32_t hi, lo;
+          split_pair(e[0], e[1], hi, lo);
+          p1[i / 8][i % 8 / 2] = hi;
+          p2[i / 8][i % 8 / 2] = lo;
+          __builtin_amdgcn_sched_barrier(0);
         }
-        uint32_t hi, lo;
-        split_pair(e[0], e[1], hi, lo);
-        p1[i / 8][i % 8 / 2] = hi;
-        p2[i / 8][i % 8 / 2] = lo;
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      };
+      if (coarse) weigh_again(std::true_type{});
+      else weigh_again(std::false_type{});
     }
     l_run += sum;
   };
